@@ -16,6 +16,10 @@
 // staging rows until the 16th token seals the block.  The CTA that finishes
 // last for a sequence (atomic ticket) publishes the new length, so every CTA
 // reads the old length first.
+//
+// A call that seals a block begun by an earlier one and leaves a new block open
+// reads and writes the same staging rows: the CTA that seals does both, in that
+// order (the open block's own CTA leaves the staging rows alone then).
 #include "ekv_internal.h"
 #include "ekv_quant.cuh"
 
@@ -51,6 +55,16 @@ append_kernel(DevState st, int layer, const int32_t* __restrict__ slots, int n_n
   const size_t in_row = (size_t)st.Hkv * D;
   const __half* kin = k + (size_t)z * n_new * in_row + (size_t)h * D;
   const __half* vin = v + (size_t)z * n_new * in_row + (size_t)h * D;
+  // The first block touched is an earlier call's and fills up, and a later one stays open.
+  const bool both = told % BLOCK != 0 && tnew / BLOCK > told / BLOCK && tnew % BLOCK != 0;
+  auto stage_rows = [&](int a, int b, int first) {  // tokens a .. b-1, of the block at `first`
+    __half* stg = st.staging + lsh_index(st, layer, slot, h) * (BLOCK * D);
+    for (int i = tid; i < (b - a) * CH; i += APPEND_THREADS) {
+      const int p = a + i / CH, cc = i % CH;
+      *reinterpret_cast<uint4*>(stg + (size_t)(p - first) * D + 8 * cc) =
+          *reinterpret_cast<const uint4*>(kin + (size_t)(p - told) * in_row + 8 * cc);
+    }
+  };
 
   if (lo < hi) {
     if (tid == 0) {
@@ -93,15 +107,15 @@ append_kernel(DevState st, int layer, const int32_t* __restrict__ slots, int n_n
           if (st.asym) seal_k<D, true>(stg, kin, in_row, j, told, kb, page, tid, st.kclip + lh * D);
           else seal_k<D, false>(stg, kin, in_row, j, told, kb, page, tid, st.kclip + lh * D);
         }
-      } else {
-        for (int i = tid; i < (hi - lo) * CH; i += APPEND_THREADS) {
-          const int p = lo + i / CH, cc = i % CH;
-          *reinterpret_cast<uint4*>(stg + (size_t)(p - j * BLOCK) * D + 8 * cc) =
-              *reinterpret_cast<const uint4*>(kin + (size_t)(p - told) * in_row + 8 * cc);
-        }
+      } else if (!both) {
+        stage_rows(lo, hi, j * BLOCK);
       }
     } else if (j * BLOCK < told) {  // an existing block must have a page
       if (tid == 0) set_error(st, EKV_ESTATE);
+    }
+    if (both && j == told / BLOCK) {  // sealed above: the rows are free for the open block
+      __syncthreads();
+      stage_rows(tnew / BLOCK * BLOCK, tnew, tnew / BLOCK * BLOCK);
     }
     // ring: the newest 64 K vectors, slot p % 64
     __half* ring = st.ring + lsh_index(st, layer, slot, h) * (RING * D);
