@@ -15,7 +15,12 @@
  * and, around them: the KIVI-style asymmetric quantizer as a per-handle option
  * (ekv_config.quantizer), and the static-artifact mode's frozen clipping
  * thresholds (ekv_set_clip), percentile select (ekv_abs_percentile) and AutoK
- * layer allocator (ekv_autok).
+ * layer allocator (ekv_autok).  For serving a model with the cache:
+ *
+ *   ekv_rope         rotary positions of q and k
+ *   ekv_prompt_attn  causal attention over packed prompts
+ *   ekv_tree_attn    attention of drafted trees over the cache
+ *   ekv_verify_tree  verification of drafted trees against the target's probabilities
  *
  * Sources of the operations (page title, section):
  *   - "EchoKV: watching a language model decide its own precision":
@@ -413,6 +418,141 @@ typedef struct ekv_stats_t {
 } ekv_stats_t;
 EKV_API int ekv_stats(ekv_cache* cache, int32_t first_layer, int32_t n_layers, ekv_stats_t* out,
                       void* stream);
+
+/* ---- Serving a model with the cache: positions, prompts and drafted tokens.
+ * A prompt goes through ekv_rope, ekv_append (its K/V into the cache) and
+ * ekv_prompt_attn; a step through ekv_rope and ekv_append_decode_attn, or, with
+ * drafted tokens, through ekv_rope, ekv_tree_attn of every layer, ekv_verify_tree
+ * and ekv_append of the accepted path.  These operators are this library's own
+ * additions around the decode path; the pages leave them to the model. */
+
+/* Rotary positions.  Pair i < rot_dim / 2 of a head's first rot_dim channels,
+ * (x_a, x_b) = channels (i, i + rot_dim/2) (EKV_ROPE_HALF) or (2i, 2i+1)
+ * (EKV_ROPE_INTERLEAVED), becomes
+ *   y_a = g (x_a cos t - x_b sin t),  y_b = g (x_b cos t + x_a sin t),
+ * t = position * f_i; the other channels are copied.  f_i = base^(-2i/rot_dim),
+ * then by `scaling` (L = original_len, w clamped to [0, 1]):
+ *   EKV_ROPE_SCALE_NONE     f
+ *   EKV_ROPE_SCALE_LINEAR   f / factor
+ *   EKV_ROPE_SCALE_BANDED   f (w + (1 - w) / factor),
+ *                           w = (L f / 2pi - low_freq_factor) / (high_freq_factor - low_freq_factor)
+ *   EKV_ROPE_SCALE_YARN     f (1 - w + w / factor), w = (i - lo) / max(hi - lo, 1e-3),
+ *                           lo = max(floor(e(beta_fast)), 0), hi = min(ceil(e(beta_slow)), rot_dim - 1),
+ *                           e(n) = rot_dim ln(L / (2pi n)) / (2 ln base)
+ * g = magnitude if that is > 0; else 0.1 ln(factor) + 1 for EKV_ROPE_SCALE_YARN
+ * with factor > 1, and 1 otherwise. */
+#define EKV_ROPE_HALF 0
+#define EKV_ROPE_INTERLEAVED 1
+#define EKV_ROPE_SCALE_NONE 0
+#define EKV_ROPE_SCALE_LINEAR 1
+#define EKV_ROPE_SCALE_BANDED 2
+#define EKV_ROPE_SCALE_YARN 3
+typedef struct ekv_rope_config {
+  int32_t head_dim;        /* 64 or 128                                                */
+  int32_t rot_dim;         /* even, 2 .. head_dim                                      */
+  int32_t layout;          /* EKV_ROPE_HALF or EKV_ROPE_INTERLEAVED                    */
+  int32_t scaling;         /* EKV_ROPE_SCALE_*                                         */
+  double base;             /* > 1                                                      */
+  double factor;           /* > 0; used by every scaling but NONE                      */
+  double original_len;     /* > 0; BANDED and YARN                                     */
+  double low_freq_factor;  /* > 0; BANDED                                              */
+  double high_freq_factor; /* > low_freq_factor; BANDED                                */
+  double beta_fast;        /* > beta_slow; YARN                                        */
+  double beta_slow;        /* > 0; YARN                                                */
+  double magnitude;        /* >= 0; 0 = the scaling's own                              */
+} ekv_rope_config;
+
+/* The frequency table of a configuration (host only): turns[i] (host
+ * uint64[rot_dim / 2]) = f_i / 2pi as a fraction of 2^64 (whole turns dropped),
+ * and the magnitude g (may be NULL). */
+EKV_API int ekv_rope_table(const ekv_rope_config* cfg, uint64_t* turns, float* magnitude);
+
+/* Rotate q and k of n_tokens tokens.
+ *   turns      dev uint64[rot_dim / 2], 8-byte aligned: ekv_rope_table's values
+ *   positions  dev int32[n_tokens] (any value; tokens may share one)
+ *   q, q_out   dev fp16: token t's heads at q + t * q_stride, [Hq][d] contiguous
+ *              (strides in elements, >= Hq * d, multiples of 8; bases 16-byte
+ *              aligned).  q_out may be q itself (same stride: in place); the
+ *              buffers must not overlap otherwise.  k, k_out: the same.
+ * A head count of 0 leaves that tensor out.  Angles are exact to 2^-32 turns at
+ * every position; the rotation is fp32, rounded once to fp16 (RNE). */
+EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t n_tokens,
+                     const int32_t* positions, int32_t n_q_heads, const void* q, int64_t q_stride,
+                     void* q_out, int64_t q_out_stride, int32_t n_kv_heads, const void* k,
+                     int64_t k_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* Causal attention over whole prompts packed end to end.
+ *   cu_seqlens  dev int32[n_seqs + 1]: sequence z holds rows cu_seqlens[z] ..
+ *               cu_seqlens[z+1] - 1 of q, k, v and o (ascending; a sequence may be
+ *               empty); rows outside every sequence are neither used nor written
+ *   q, o        dev fp16, token t's heads at q + t * q_stride, [Hq][d] contiguous
+ *   k, v        the same with [Hkv][d]; strides in elements, multiples of 8, at
+ *               least a token's heads; bases 16-byte aligned
+ * o_ih = sum_{j <= i} softmax_j(scale q_ih . k_jg) v_jg over i's sequence,
+ * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d).  fp32 accumulation, the
+ * probabilities rounded to fp16 before they multiply V, o rounded to fp16 (RNE).
+ * head_dim 64 or 128 (else EKV_EUNSUPPORTED).  total_tokens: rows of every
+ * buffer; bounds outside [0, total_tokens] or descending leave that sequence out. */
+EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                            float softmax_scale, int32_t total_tokens, int32_t n_seqs,
+                            const int32_t* cu_seqlens, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            void* o, int64_t o_stride, void* stream);
+
+/* Attention of drafted trees over the cache (one layer).  A sequence's tree has
+ * n_nodes[z] nodes; node i's parent is parents[z][i] < i, or -1 (any other value
+ * is read as -1).  Nodes are not in the cache: their K/V are given here, raw, and
+ * the cache is only read.
+ *   max_nodes  1 .. EKV_TREE_MAX_NODES: the row count of every array below
+ *   n_nodes    dev int32[n_seqs], NULL = max_nodes each (values above it are cut);
+ *              rows of o behind a sequence's nodes are left as they were
+ *   parents    dev int32[n_seqs][max_nodes]
+ *   q, o       dev fp16 [n_seqs][max_nodes][Hq][d]
+ *   k, v       dev fp16 [n_seqs][max_nodes][Hkv][d]; all four 16-byte aligned
+ * o_ih = softmax-weighted sum over every cached token of the sequence (the
+ * dequantized page values, as ekv_decode_attn) and over the k, v of node i and
+ * its ancestors.  A sequence may have no cached tokens.
+ *   scratch    dev, 16-byte aligned, ekv_tree_attn_scratch_bytes bytes
+ *              (caller-owned; overwritten; one call at a time)
+ * Device errors as ekv_decode_attn. */
+#define EKV_TREE_MAX_NODES 64
+EKV_API int ekv_tree_attn(ekv_cache* cache, int32_t layer, int32_t n_seqs,
+                          const int32_t* seq_slots, int32_t max_nodes, const int32_t* n_nodes,
+                          const int32_t* parents, const void* q, const void* k, const void* v,
+                          void* o, void* scratch, int64_t scratch_bytes, void* stream);
+/* Scratch bytes of ekv_tree_attn for any layer of a handle (host only). */
+EKV_API int ekv_tree_attn_scratch_bytes(ekv_cache* cache, int32_t n_seqs, int32_t max_nodes,
+                                        int64_t* out);
+
+/* Verification of drafted trees.  Node 0 of a tree is its root (the last
+ * committed token); parents[z][i] in 0 .. i-1 (a node with any other parent is
+ * never reached).  From the root, the children c of the current node u are tried in
+ * index order, starting with r = p_u, Z = 1:
+ *   accept c iff u_accept[c] q(x_c) Z < r(x_c)   (x_c = tokens[c])
+ *   else r <- max(r - Z q, 0), Z <- sum r
+ * with q = q_u, the draft distribution u's children were sampled from.  Without
+ * draft_probs a child is taken as certain to be drafted (q(x_c) = 1): a rejection
+ * takes x_c's mass out, Z <- Z - r(x_c), r(x_c) <- 0.  An accepted child becomes
+ * the current node; when none is accepted, next_token is the lowest index i with
+ * cum_i(r) > u_sample sum(r) (r = p_u if sum(r) is 0).
+ *   target_probs  dev fp32: p after node i of sequence z at
+ *                 z * target_seq_stride + i * target_row_stride, [vocab] (strides
+ *                 in elements; row stride >= vocab); draft_probs likewise or NULL
+ *   tokens, parents  dev int32 [n_seqs][max_nodes] (tokens[z][0] is not used);
+ *                 a token outside the vocabulary is never accepted
+ *   n_nodes       dev int32[n_seqs] or NULL (max_nodes each)
+ *   u_accept      dev fp32 [n_seqs][max_nodes] in [0, 1); u_sample [n_seqs]
+ *   path          dev int32 [n_seqs][max_nodes]: accepted nodes in order, then -1
+ *   n_accept, next_token  dev int32 [n_seqs] (0 and -1 where n_nodes <= 0)
+ * Entries of a row count as fixed point in units of 2^-60, clamped to [0, 1] (NaN
+ * as 0); a row must sum to less than 4. */
+EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_t vocab,
+                            const float* target_probs, int64_t target_seq_stride,
+                            int64_t target_row_stride, const float* draft_probs,
+                            int64_t draft_seq_stride, int64_t draft_row_stride,
+                            const int32_t* tokens, const int32_t* parents,
+                            const int32_t* n_nodes, const float* u_accept, const float* u_sample,
+                            int32_t* path, int32_t* n_accept, int32_t* next_token, void* stream);
 
 /* Free pages left in the pool of one format (syncs stream). */
 EKV_API int ekv_pool_free(ekv_cache* cache, int32_t format, int64_t* out, void* stream);

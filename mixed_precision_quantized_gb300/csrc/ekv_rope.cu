@@ -1,0 +1,247 @@
+// ekv_rope.cu — rotary positions of q and k before the append and the attention.
+//
+// Pair i of a head's first r channels, (x_a, x_b) = (i, i + r/2) (half layout) or
+// (2i, 2i+1) (interleaved), turns by the angle t = pos * f_i:
+//   y_a = g (x_a cos t - x_b sin t),  y_b = g (x_b cos t + x_a sin t)
+// and the other d - r channels pass through.  f_i = base^(-2i/r), changed for
+// long contexts by the configured scaling; g is the scaling's magnitude.
+//
+// The angle is kept in turns as a 64-bit fixed-point fraction: the table holds
+// F_i = round(f_i / 2pi * 2^64), and pos * F_i mod 2^64 is the fraction of a
+// turn, exact in the product for every int32 position (the table's rounding
+// moves the angle by at most 2^31 * 2^-65 turns).  Its top 32 bits go to fp32
+// and through sincospif, so a far position loses nothing to range reduction and
+// no fp64 arithmetic is spent.  The rotation is done in fp32 and rounded to
+// fp16 once.
+//
+// Bound by memory: each q and k element is read and written once.  A CTA takes a
+// few tokens; its threads first fill a shared table of cos and sin, one entry
+// per (token, pair), which all q and k heads of the token share, then rotate
+// 8 pairs (half layout) or 4 pairs (interleaved) per step in 16-byte accesses.
+#include <math.h>
+
+#include "ekv_internal.h"
+
+namespace ekv {
+namespace {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_MAX_TOKENS = 8;   // tokens of one CTA at most
+constexpr int ROPE_MAX_PAIRS = 64;   // head_dim / 2
+
+struct RopeArgs {
+  const uint64_t* turns;
+  const int32_t* pos;
+  const __half* x[2];   // q, k
+  __half* y[2];
+  int64_t xs[2], ys[2];  // token strides (elements)
+  int heads[2];
+  int64_t n;
+  int d, rot, tokens;    // tokens per CTA
+  float mag;
+};
+
+__device__ __forceinline__ void rotate2(uint32_t& a, uint32_t& b, float2 w0, float2 w1) {
+  // a = (x_a0, x_a1), b = (x_b0, x_b1) of two pairs
+  const float2 fa = __half22float2(*reinterpret_cast<__half2*>(&a));
+  const float2 fb = __half22float2(*reinterpret_cast<__half2*>(&b));
+  const __half2 ra = __floats2half2_rn(fa.x * w0.x - fb.x * w0.y, fa.y * w1.x - fb.y * w1.y);
+  const __half2 rb = __floats2half2_rn(fb.x * w0.x + fa.x * w0.y, fb.y * w1.x + fa.y * w1.y);
+  a = *reinterpret_cast<const uint32_t*>(&ra);
+  b = *reinterpret_cast<const uint32_t*>(&rb);
+}
+__device__ __forceinline__ uint32_t rotate1(uint32_t ab, float2 w) {  // (x_a, x_b) of one pair
+  const float2 f = __half22float2(*reinterpret_cast<__half2*>(&ab));
+  const __half2 r = __floats2half2_rn(f.x * w.x - f.y * w.y, f.y * w.x + f.x * w.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// MODE 0: half layout, r a multiple of 16 (16-byte accesses); 1: interleaved, r a
+// multiple of 8 (16-byte accesses); 2 / 3: half / interleaved for any even r, one
+// pair at a time.
+template <int MODE>
+__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeArgs A) {
+  __shared__ float2 s_w[ROPE_MAX_TOKENS * ROPE_MAX_PAIRS];
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * A.tokens;
+  const int nt = (int)min((int64_t)A.tokens, A.n - t0);
+  const int half = A.rot / 2;
+  for (int i = tid; i < nt * half; i += ROPE_THREADS) {
+    const int t = i / half, p = i - t * half;
+    const uint64_t frac = (uint64_t)(int64_t)A.pos[t0 + t] * A.turns[p];
+    float s, c;
+    sincospif((float)(int32_t)(frac >> 32) * 0x1p-31f, &s, &c);  // 2 pi frac = pi (2 frac)
+    s_w[t * ROPE_MAX_PAIRS + p] = make_float2(c * A.mag, s * A.mag);
+  }
+  __syncthreads();
+  constexpr bool VEC = MODE < 2;
+  // Units of one head: rotated ones, then (16-byte or single-channel) copies.
+  const int ru = MODE == 0 ? A.rot / 16 : MODE == 1 ? A.rot / 8 : half;
+  const int cu = VEC ? (A.d - A.rot) / 8 : A.d - A.rot;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int H = A.heads[which];
+    if (H == 0) continue;
+    const __half* x = A.x[which];
+    __half* y = A.y[which];
+    const int per = H * (ru + cu);
+    for (int i = tid; i < nt * per; i += ROPE_THREADS) {
+      const int t = i / per, r = i - t * per;
+      const int h = r / (ru + cu), u = r - h * (ru + cu);
+      const __half* src = x + (t0 + t) * A.xs[which] + (size_t)h * A.d;
+      __half* dst = y + (t0 + t) * A.ys[which] + (size_t)h * A.d;
+      const float2* w = s_w + t * ROPE_MAX_PAIRS;
+      if (u >= ru) {
+        const int c = A.rot + (u - ru) * (VEC ? 8 : 1);
+        if (src != dst) {
+          if (VEC) *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
+          else dst[c] = src[c];
+        }
+      } else if (MODE == 0) {
+        uint4 a = *reinterpret_cast<const uint4*>(src + 8 * u);
+        uint4 b = *reinterpret_cast<const uint4*>(src + half + 8 * u);
+        const float2* wu = w + 8 * u;
+        rotate2(a.x, b.x, wu[0], wu[1]);
+        rotate2(a.y, b.y, wu[2], wu[3]);
+        rotate2(a.z, b.z, wu[4], wu[5]);
+        rotate2(a.w, b.w, wu[6], wu[7]);
+        *reinterpret_cast<uint4*>(dst + 8 * u) = a;
+        *reinterpret_cast<uint4*>(dst + half + 8 * u) = b;
+      } else if (MODE == 1) {
+        uint4 a = *reinterpret_cast<const uint4*>(src + 8 * u);
+        const float2* wu = w + 4 * u;
+        a.x = rotate1(a.x, wu[0]);
+        a.y = rotate1(a.y, wu[1]);
+        a.z = rotate1(a.z, wu[2]);
+        a.w = rotate1(a.w, wu[3]);
+        *reinterpret_cast<uint4*>(dst + 8 * u) = a;
+      } else {
+        const int ia = MODE == 2 ? u : 2 * u, ib = MODE == 2 ? u + half : 2 * u + 1;
+        const float fa = __half2float(src[ia]), fb = __half2float(src[ib]);
+        dst[ia] = __float2half_rn(fa * w[u].x - fb * w[u].y);
+        dst[ib] = __float2half_rn(fb * w[u].x + fa * w[u].y);
+      }
+    }
+  }
+}
+
+bool valid_config(const ekv_rope_config* c) {
+  if (!c || (c->head_dim != 64 && c->head_dim != 128)) return false;
+  if (c->rot_dim < 2 || c->rot_dim > c->head_dim || (c->rot_dim & 1)) return false;
+  if (c->layout != EKV_ROPE_HALF && c->layout != EKV_ROPE_INTERLEAVED) return false;
+  if (c->scaling < EKV_ROPE_SCALE_NONE || c->scaling > EKV_ROPE_SCALE_YARN) return false;
+  if (!(c->base > 1.0) || !isfinite(c->base)) return false;
+  if (!(c->magnitude >= 0.0) || !isfinite(c->magnitude)) return false;
+  if (c->scaling != EKV_ROPE_SCALE_NONE && (!(c->factor > 0.0) || !isfinite(c->factor)))
+    return false;
+  if (c->scaling == EKV_ROPE_SCALE_BANDED || c->scaling == EKV_ROPE_SCALE_YARN) {
+    if (!(c->original_len > 0.0) || !isfinite(c->original_len)) return false;
+  }
+  if (c->scaling == EKV_ROPE_SCALE_BANDED &&
+      !(c->low_freq_factor > 0.0 && c->high_freq_factor > c->low_freq_factor &&
+        isfinite(c->high_freq_factor)))
+    return false;
+  if (c->scaling == EKV_ROPE_SCALE_YARN &&
+      !(c->beta_slow > 0.0 && c->beta_fast > c->beta_slow && isfinite(c->beta_fast)))
+    return false;
+  return true;
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+float magnitude_of(const ekv_rope_config& c) {
+  if (c.magnitude > 0.0) return (float)c.magnitude;
+  return c.scaling == EKV_ROPE_SCALE_YARN && c.factor > 1.0 ? (float)(0.1 * log(c.factor) + 1.0)
+                                                            : 1.f;
+}
+
+double freq_of(const ekv_rope_config& c, int i) {
+  const int r = c.rot_dim;
+  const double f = pow(c.base, -2.0 * i / r);
+  switch (c.scaling) {
+    case EKV_ROPE_SCALE_LINEAR: return f / c.factor;
+    case EKV_ROPE_SCALE_BANDED: {
+      const double turns = c.original_len * f / kTwoPi;  // over the original context
+      double w = (turns - c.low_freq_factor) / (c.high_freq_factor - c.low_freq_factor);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      return f * (w + (1.0 - w) / c.factor);
+    }
+    case EKV_ROPE_SCALE_YARN: {
+      // the pair index at which the original context holds `turns` turns
+      auto edge = [&](double turns) {
+        return r * log(c.original_len / (turns * kTwoPi)) / (2.0 * log(c.base));
+      };
+      const double lo = fmax(floor(edge(c.beta_fast)), 0.0);
+      const double hi = fmin(ceil(edge(c.beta_slow)), r - 1.0);
+      double w = (i - lo) / fmax(hi - lo, 1e-3);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      return f * (1.0 - w + w / c.factor);
+    }
+    default: return f;
+  }
+}
+
+}  // namespace
+}  // namespace ekv
+
+extern "C" EKV_API int ekv_rope_table(const ekv_rope_config* cfg, uint64_t* turns,
+                                      float* magnitude) {
+  using namespace ekv;
+  if (!valid_config(cfg) || !turns) return EKV_EINVAL;
+  for (int i = 0; i < cfg->rot_dim / 2; ++i) {
+    double t = freq_of(*cfg, i) / kTwoPi;
+    t -= floor(t);  // whole turns do not matter
+    // t < 1 in doubles, so t * 2^64 < 2^64; split so that the conversion is exact
+    const uint64_t hi = (uint64_t)(t * 0x1p32);
+    turns[i] = (hi << 32) + (uint64_t)((t * 0x1p32 - (double)hi) * 0x1p32);
+  }
+  if (magnitude) *magnitude = magnitude_of(*cfg);
+  return EKV_OK;
+}
+
+extern "C" EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t n_tokens,
+                                const int32_t* positions, int32_t n_q_heads, const void* q,
+                                int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                int32_t n_kv_heads, const void* k, int64_t k_stride, void* k_out,
+                                int64_t k_out_stride, void* stream) {
+  using namespace ekv;
+  if (!valid_config(cfg) || n_tokens < 0 || n_tokens > 0x7FFFFFFF || n_q_heads < 0 ||
+      n_kv_heads < 0 || n_q_heads > 4096 || n_kv_heads > 4096)
+    return EKV_EINVAL;
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return EKV_OK;
+  if (!turns || !positions || ((uintptr_t)turns & 7) || ((uintptr_t)positions & 3))
+    return EKV_EINVAL;
+  RopeArgs A = {};
+  const int heads[2] = {n_q_heads, n_kv_heads};
+  const void* xs[2] = {q, k};
+  void* ys[2] = {q_out, k_out};
+  const int64_t xst[2] = {q_stride, k_stride}, yst[2] = {q_out_stride, k_out_stride};
+  for (int w = 0; w < 2; ++w) {
+    A.heads[w] = heads[w];
+    if (heads[w] == 0) continue;
+    const int64_t row = (int64_t)heads[w] * cfg->head_dim;
+    if (!xs[w] || !ys[w] || (((uintptr_t)xs[w] | (uintptr_t)ys[w]) & 15)) return EKV_EINVAL;
+    if (xst[w] < row || yst[w] < row || ((xst[w] | yst[w]) & 7)) return EKV_EINVAL;
+    if (xs[w] == ys[w] && xst[w] != yst[w]) return EKV_EINVAL;  // in place: the same rows
+    A.x[w] = static_cast<const __half*>(xs[w]);
+    A.y[w] = static_cast<__half*>(ys[w]);
+    A.xs[w] = xst[w];
+    A.ys[w] = yst[w];
+  }
+  A.turns = turns;
+  A.pos = positions;
+  A.n = n_tokens;
+  A.d = cfg->head_dim;
+  A.rot = cfg->rot_dim;
+  A.mag = magnitude_of(*cfg);
+  A.tokens = n_tokens >= 2048 ? 4 : 1;
+  const int64_t grid = (n_tokens + A.tokens - 1) / A.tokens;
+  const bool inter = cfg->layout == EKV_ROPE_INTERLEAVED;
+  const bool vec = A.rot % (inter ? 8 : 16) == 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (vec && !inter) rope_kernel<0><<<(unsigned)grid, ROPE_THREADS, 0, s>>>(A);
+  else if (vec) rope_kernel<1><<<(unsigned)grid, ROPE_THREADS, 0, s>>>(A);
+  else if (!inter) rope_kernel<2><<<(unsigned)grid, ROPE_THREADS, 0, s>>>(A);
+  else rope_kernel<3><<<(unsigned)grid, ROPE_THREADS, 0, s>>>(A);
+  return cudaGetLastError() == cudaSuccess ? EKV_OK : EKV_ECUDA;
+}

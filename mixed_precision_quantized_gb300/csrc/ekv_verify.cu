@@ -1,0 +1,331 @@
+// ekv_verify.cu — verification of drafted trees against the target's probabilities.
+//
+// A sequence's tree has nodes 0 .. cnt-1, node 0 the root (the last committed
+// token), parents[i] < i; p_u is the target's distribution after node u, and q_u
+// (optional) the draft distribution that u's children were sampled from.  From
+// the root, the children c of the current node are tried in index order with
+// r = p_u, Z = 1:
+//   accept c iff  u_c q(x_c) Z < r(x_c)            (without q: q(x_c) = 1)
+//   else          r <- max(r - Z q, 0), Z <- sum r (without q: Z <- Z - r(x_c), r(x_c) <- 0)
+// An accepted child becomes the current node.  At a node with no accepted child the
+// walk ends and the next token is the lowest index i with cum_i(r) > u_s sum r; if
+// sum r = 0 it is drawn from p_u.  Every token is then distributed as the target's.
+//
+// Sums over the vocabulary are exact: probabilities go to unsigned 64-bit fixed
+// point in units of 2^-60 (an fp32 value above 2^-36 converts without loss), whose
+// sums do not depend on their order, so the sampled index is the same on every
+// launch.  Decisions compare one product in fp64.
+//
+// Only the gathered p(x_c), q(x_c) of the drafted nodes are read for the walk, all
+// at once; whole rows are read only where the residual is needed: the last node's p
+// (and q), and with q each node at which a child was rejected.  Bound by latency:
+// one launch, one round of gathers, one pass over the last row.  A cluster of CL
+// CTAs shares a sequence's row passes, exchanging partial sums through distributed
+// shared memory.
+#include <cooperative_groups.h>
+
+#include "ekv_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace ekv {
+namespace {
+
+constexpr int VT = 512;          // threads per CTA
+constexpr int VWARPS = VT / 32;
+constexpr int VMAX = EKV_TREE_MAX_NODES;
+
+struct VerifyArgs {
+  const float* p;
+  const float* q;
+  int64_t p_seq, p_row, q_seq, q_row;
+  const int32_t *tokens, *parents, *n_nodes;
+  const float *u, *us;
+  int32_t *path, *n_accept, *next;
+  int m, vocab, vec;
+};
+
+// 2^60 x for x in [0, 1] (clamped; negative and NaN: 0), truncated.
+__device__ __forceinline__ uint64_t fix60(float x) {
+  x = x > 0.f ? fminf(x, 1.f) : 0.f;
+  return __float2ull_rz(x * 0x1p60f);
+}
+// a * z in units of 2^-60, a < 2^62 and z < 2^62 (saturated by the caller).
+__device__ __forceinline__ uint64_t mul60(uint64_t a, uint64_t z) {
+  return __umul64hi(a << 2, z << 2);
+}
+// The residual after k rejections with draft probabilities: z[j] is Z before
+// rejection j (z[0] = 1, taken exactly).
+__device__ __forceinline__ uint64_t residual(uint64_t r, uint64_t q, const uint64_t* z, int k) {
+  for (int j = 0; j < k; ++j) {
+    const uint64_t cut = j == 0 ? q : mul60(q, z[j]);
+    r = r > cut ? r - cut : 0;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void load4(const float* row, int i, int n, int vec, float* f) {
+  if (vec && i + 4 <= n) {
+    const float4 t = *reinterpret_cast<const float4*>(row + i);
+    f[0] = t.x; f[1] = t.y; f[2] = t.z; f[3] = t.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = i + j < n ? row[i + j] : 0.f;
+  }
+}
+
+template <int CL>
+__global__ void __launch_bounds__(VT) verify_kernel(VerifyArgs A) {
+  __shared__ int s_par[VMAX], s_tok[VMAX], s_path[VMAX], s_gone[VMAX];
+  __shared__ float s_u[VMAX], s_p[VMAX], s_q[VMAX];
+  __shared__ uint64_t s_wsum[VWARPS], s_part[2][CL], s_z[VMAX];
+  const int z = blockIdx.x / CL, rank = blockIdx.x % CL;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int V = A.vocab;
+  const int cnt = A.n_nodes ? min(A.m, A.n_nodes[z]) : A.m;
+  const float* P = A.p + z * A.p_seq;
+  const float* Q = A.q ? A.q + z * A.q_seq : nullptr;
+  if (tid < cnt) {
+    const int par = tid ? A.parents[(size_t)z * A.m + tid] : -1;
+    const int tok = A.tokens[(size_t)z * A.m + tid];
+    // a bad parent or a token outside the vocabulary: no one's child
+    const bool ok = tid > 0 && par >= 0 && par < tid && tok >= 0 && tok < V;
+    s_par[tid] = ok ? par : -1;
+    s_tok[tid] = tok;
+    s_u[tid] = A.u[(size_t)z * A.m + tid];
+    s_p[tid] = ok ? P[par * A.p_row + tok] : 0.f;
+    s_q[tid] = ok && Q ? Q[par * A.q_row + tok] : 1.f;
+  }
+  __syncthreads();
+
+  // The slice of a row that this CTA sums, and each warp's chunk of it, in units
+  // of 128 elements (one 16-byte load per lane): contiguous, in order.
+  const int units = (V + 127) / 128;
+  const int per_warp = (units + CL * VWARPS - 1) / (CL * VWARPS);
+  const int u0 = min(units, (rank * VWARPS + warp) * per_warp);
+  const int u1 = min(units, u0 + per_warp);
+  int flip = 0;
+  // Sum of the residual over the whole row: node's p (and q) after k rejections
+  // (with q), or with the tokens s_gone[0 .. ngone) taken out (without).  Every
+  // thread of the cluster returns the total; s_wsum holds this CTA's chunk sums,
+  // s_part[flip ^ 1] all CTAs' sums.
+  auto row_sum = [&](int node, int k, int ngone) -> uint64_t {
+    const float* pr = P + node * A.p_row;
+    const float* qr = Q ? Q + node * A.q_row : nullptr;
+    uint64_t sum = 0;
+    for (int t = u0; t < u1; ++t) {
+      float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+      load4(pr, t * 128 + lane * 4, V, A.vec, a);
+      if (k) load4(qr, t * 128 + lane * 4, V, A.vec, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += residual(fix60(a[j]), fix60(b[j]), s_z, k);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_wsum[warp] = sum;
+    __syncthreads();
+    if (tid < ngone) {  // distinct tokens, each in one warp's chunk
+      const int x = s_gone[tid], w = x / 128 / per_warp - rank * VWARPS;
+      if (w >= 0 && w < VWARPS)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s_wsum[w]),
+                  (unsigned long long)(0 - fix60(pr[x])));
+    }
+    __syncthreads();
+    if (tid < CL) {
+      uint64_t mine = 0;
+      for (int w = 0; w < VWARPS; ++w) mine += s_wsum[w];
+      if (CL == 1) s_part[flip][0] = mine;
+      else *cg::this_cluster().map_shared_rank(&s_part[flip][rank], tid) = mine;
+    }
+    if (CL == 1) __syncthreads();
+    else cg::this_cluster().sync();
+    uint64_t total = 0;
+    for (int r = 0; r < CL; ++r) total += s_part[flip][r];
+    flip ^= 1;
+    return total;
+  };
+
+  // The walk, the same in every thread of the cluster.
+  int node = 0, nacc = 0, k = 0, ngone = 0;
+  uint64_t total = 0;
+  bool have = false;  // `total` is the residual's sum at the current node
+  if (cnt > 0) {
+    double left = 1.0;
+    for (int c = 1; c < cnt; ++c) {
+      if (s_par[c] != node) continue;
+      const int x = s_tok[c];
+      double r;
+      if (!Q) {
+        bool twin = false;
+        for (int j = 0; j < ngone; ++j) twin |= s_gone[j] == x;
+        r = twin ? 0.0 : (double)s_p[c];
+      } else {
+        r = k == 0 ? (double)s_p[c]
+                   : (double)residual(fix60(s_p[c]), fix60(s_q[c]), s_z, k) * 0x1p-60;
+      }
+      if ((double)s_u[c] * (double)s_q[c] * left < r) {
+        if (tid == 0) s_path[nacc] = c;
+        ++nacc;
+        node = c;
+        k = ngone = 0;
+        left = 1.0;
+        have = false;
+        continue;
+      }
+      if (!Q) {
+        left -= r;
+        bool twin = false;
+        for (int j = 0; j < ngone; ++j) twin |= s_gone[j] == x;
+        if (!twin) {
+          __syncthreads();
+          if (tid == 0) s_gone[ngone] = x;
+          ++ngone;
+          __syncthreads();
+        }
+      } else {
+        __syncthreads();
+        if (tid == 0) s_z[k] = k == 0 ? 1ull << 60 : min(total, (uint64_t)((1ull << 62) - 1));
+        ++k;
+        __syncthreads();
+        total = row_sum(node, k, 0);
+        have = true;
+        left = (double)total * 0x1p-60;
+      }
+    }
+  }
+
+  int next = -1;
+  if (cnt > 0) {
+    if (!have) total = row_sum(node, k, ngone);
+    if (total == 0 && (k > 0 || ngone > 0)) {
+      k = ngone = 0;
+      total = row_sum(node, 0, 0);
+    }
+    next = V - 1;  // an all-zero row
+    if (total > 0) {
+      const float us = A.us[z];
+      const uint64_t frac = us >= 1.f ? ~0ull : us > 0.f ? __float2ull_rz(us * 0x1p64f) : 0ull;
+      const uint64_t target = __umul64hi(frac, total);  // floor(u_s * sum r) < sum r
+      uint64_t base = 0;
+      for (int r = 0; r < rank; ++r) base += s_part[flip ^ 1][r];
+      for (int w = 0; w < warp; ++w) base += s_wsum[w];
+      next = -1;
+      if (target >= base && target - base < s_wsum[warp]) {  // this warp's chunk holds it
+        const float* pr = P + node * A.p_row;
+        const float* qr = Q ? Q + node * A.q_row : nullptr;
+        for (int t = u0; t < u1; ++t) {
+          float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+          const int i0 = t * 128 + lane * 4;
+          load4(pr, i0, V, A.vec, a);
+          if (k) load4(qr, i0, V, A.vec, b);
+          uint64_t e[4], s = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = residual(fix60(a[j]), fix60(b[j]), s_z, k);
+            for (int g = 0; g < ngone; ++g)
+              if (s_gone[g] == i0 + j) e[j] = 0;
+            s += e[j];
+          }
+          uint64_t inc = s;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, base + inc > target);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) {
+              uint64_t cum = base + inc - s;
+              for (int j = 0; j < 4; ++j) {
+                cum += e[j];
+                if (cum > target) {
+                  A.next[z] = i0 + j;
+                  break;
+                }
+              }
+            }
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (rank == 0) {
+    if (tid < A.m) A.path[(size_t)z * A.m + tid] = tid < nacc ? s_path[tid] : -1;
+    if (tid == 0) {
+      A.n_accept[z] = nacc;
+      if (cnt <= 0) A.next[z] = -1;
+      else if (total == 0) A.next[z] = V - 1;
+    }
+  }
+  if (CL > 1) cg::this_cluster().sync();  // no CTA leaves while another may write its sums
+}
+
+template <int CL>
+cudaError_t launch_verify(const VerifyArgs& A, int n_seqs, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_seqs * CL);
+  cfg.blockDim = dim3(VT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<CL>, A);
+}
+
+}  // namespace
+}  // namespace ekv
+
+extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_t vocab,
+                                       const float* target_probs, int64_t target_seq_stride,
+                                       int64_t target_row_stride, const float* draft_probs,
+                                       int64_t draft_seq_stride, int64_t draft_row_stride,
+                                       const int32_t* tokens, const int32_t* parents,
+                                       const int32_t* n_nodes, const float* u_accept,
+                                       const float* u_sample, int32_t* path, int32_t* n_accept,
+                                       int32_t* next_token, void* stream) {
+  using namespace ekv;
+  if (n_seqs < 0 || n_seqs > (1 << 20) || max_nodes < 1 || max_nodes > EKV_TREE_MAX_NODES ||
+      vocab < 1)
+    return EKV_EINVAL;
+  if (n_seqs == 0) return EKV_OK;
+  if (!target_probs || !tokens || !parents || !u_accept || !u_sample || !path || !n_accept ||
+      !next_token)
+    return EKV_EINVAL;
+  if (((uintptr_t)target_probs | (uintptr_t)draft_probs | (uintptr_t)tokens | (uintptr_t)parents |
+       (uintptr_t)n_nodes | (uintptr_t)u_accept | (uintptr_t)u_sample | (uintptr_t)path |
+       (uintptr_t)n_accept | (uintptr_t)next_token) & 3)
+    return EKV_EINVAL;
+  if ((max_nodes > 1 && target_row_stride < vocab) || (n_seqs > 1 && target_seq_stride < 0))
+    return EKV_EINVAL;
+  if (draft_probs && ((max_nodes > 1 && draft_row_stride < vocab) ||
+                      (n_seqs > 1 && draft_seq_stride < 0)))
+    return EKV_EINVAL;
+  VerifyArgs A = {};
+  A.p = target_probs;
+  A.q = draft_probs;
+  A.p_seq = target_seq_stride;
+  A.p_row = target_row_stride;
+  A.q_seq = draft_seq_stride;
+  A.q_row = draft_row_stride;
+  A.tokens = tokens;
+  A.parents = parents;
+  A.n_nodes = n_nodes;
+  A.u = u_accept;
+  A.us = u_sample;
+  A.path = path;
+  A.n_accept = n_accept;
+  A.next = next_token;
+  A.m = max_nodes;
+  A.vocab = vocab;
+  A.vec = !(((uintptr_t)target_probs | (uintptr_t)draft_probs) & 15) &&
+          !((target_seq_stride | target_row_stride) & 3) &&
+          (!draft_probs || !((draft_seq_stride | draft_row_stride) & 3));
+  const cudaError_t e = launch_verify<1>(A, n_seqs, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EKV_OK : EKV_ECUDA;
+}

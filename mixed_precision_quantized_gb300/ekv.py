@@ -7,6 +7,7 @@ built, `lib()` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -63,11 +64,29 @@ class EkvStats(ctypes.Structure):
     ]
 
 
+class EkvRopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_double),
+        ("low_freq_factor", ctypes.c_double),
+        ("high_freq_factor", ctypes.c_double),
+        ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_void_p)
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _SIGS = {
     "ekv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ekv_page_bytes": (_I32, [_I32, _I32, _I32]),
@@ -102,6 +121,16 @@ _SIGS = {
                                           ctypes.c_int64, _P]),
     "ekv_abs_percentile_scratch_bytes": (ctypes.c_int, [_I32, _P]),
     "ekv_autok": (ctypes.c_int, [_P, _I32, ctypes.c_double, _P, _P]),
+    "ekv_rope_table": (ctypes.c_int, [ctypes.POINTER(EkvRopeConfig), _P, _P]),
+    "ekv_rope": (ctypes.c_int, [ctypes.POINTER(EkvRopeConfig), _P, _I64, _P, _I32, _P, _I64, _P,
+                                _I64, _I32, _P, _I64, _P, _I64, _P]),
+    "ekv_prompt_attn": (ctypes.c_int, [_I32, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _P, _I64,
+                                       _P, _I64, _P, _I64, _P, _I64, _P]),
+    "ekv_tree_attn": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _I64,
+                                     _P]),
+    "ekv_tree_attn_scratch_bytes": (ctypes.c_int, [_P, _I32, _I32, _P]),
+    "ekv_verify_tree": (ctypes.c_int, [_I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _P,
+                                       _P, _P, _P, _P, _P, _P, _P]),
     "ekv_output_error": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P]),
 }
 EXPORTS = tuple(_SIGS)
@@ -152,6 +181,44 @@ def _ptr(t: torch.Tensor | None):
 def _stream(stream) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Make the device (and the stream, if one is given) current, so that what the
+    binding allocates belongs to the stream the call runs on; yields its handle."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device=None,
+          contiguous: bool = True):
+    """Check a tensor argument: type, shape (None: any extent), device, layout."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must have shape [{want}], got {list(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_stride(name: str, t: torch.Tensor) -> int:
+    """Token stride (elements) of [tokens, heads, d] whose heads are contiguous."""
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else max(h * d, 8)
 
 
 class Cache:
@@ -255,6 +322,39 @@ class Cache:
         _check(lib().ekv_decode_attn_noalloc(self._h, layer, seq_slots.numel(), _ptr(seq_slots),
                                              _ptr(q), _ptr(out), _stream(stream)),
                "ekv_decode_attn_noalloc")
+        return out
+
+    def tree_attn(self, layer: int, seq_slots: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                  v: torch.Tensor, parents: torch.Tensor, n_nodes: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of drafted trees over the cache (ekv_tree_attn): q [n, m, Hq, d] and
+        the nodes' own k, v [n, m, Hkv, d] (fp16, not in the cache), parents [n, m]
+        int32 (parent < node, -1 = none), n_nodes [n] int32 (None: m each).  Every
+        node attends over all cached tokens, itself and its ancestors.  Rows of
+        `out` behind a sequence's nodes are left as they were (a new `out` starts
+        at zero there)."""
+        n, H, d = seq_slots.numel(), self.num_kv_heads, self.head_dim
+        dev = seq_slots.device
+        _need("seq_slots", seq_slots, torch.int32, (n,))
+        _need("q", q, torch.float16, (n, None, self.num_q_heads, d), dev)
+        m = q.shape[1]
+        _need("k", k, torch.float16, (n, m, H, d), dev)
+        _need("v", v, torch.float16, (n, m, H, d), dev)
+        _need("parents", parents, torch.int32, (n, m), dev)
+        if n_nodes is not None:
+            _need("n_nodes", n_nodes, torch.int32, (n,), dev)
+        if out is not None:
+            _need("out", out, torch.float16, tuple(q.shape), dev)
+        with _on(dev, stream) as s:
+            if out is None:
+                out = torch.empty_like(q) if n_nodes is None else torch.zeros_like(q)
+            nb = ctypes.c_int64(0)
+            _check(lib().ekv_tree_attn_scratch_bytes(self._h, n, m, ctypes.byref(nb)),
+                   "ekv_tree_attn_scratch_bytes")
+            scratch = torch.empty(max(16, nb.value), dtype=torch.uint8, device=dev)
+            _check(lib().ekv_tree_attn(self._h, layer, n, _ptr(seq_slots), m, _ptr(n_nodes),
+                                       _ptr(parents), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                       _ptr(scratch), nb.value, s), "ekv_tree_attn")
         return out
 
     def canary_kl(self, layer: int, seq_slots: torch.Tensor, q: torch.Tensor,
@@ -381,6 +481,143 @@ class Cache:
 
     def load_state(self, blob: bytes, stream=None):
         _check(lib().ekv_state_load(self._h, blob, len(blob), _stream(stream)), "ekv_state_load")
+
+
+class Rope:
+    """Rotary positions (ekv_rope) of one configuration; holds the frequency table.
+    layout "half" (pairs i, i + rot_dim/2) or "interleaved" (2i, 2i+1); scaling
+    None or "none", "linear", "banded" or "yarn" (see ekv_rope_config)."""
+
+    LAYOUTS = {"half": 0, "interleaved": 1}
+    SCALINGS = {None: 0, "none": 0, "linear": 1, "banded": 2, "yarn": 3}
+
+    def __init__(self, head_dim: int, rot_dim: int | None = None, layout: str = "half",
+                 base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                 original_len: float = 0.0, low_freq_factor: float = 1.0,
+                 high_freq_factor: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 magnitude: float = 0.0, device=None):
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+        c = EkvRopeConfig()
+        c.head_dim, c.rot_dim = int(head_dim), int(head_dim if rot_dim is None else rot_dim)
+        c.layout, c.scaling = self.LAYOUTS[layout], self.SCALINGS[scaling]
+        c.base, c.factor, c.original_len = float(base), float(factor), float(original_len)
+        c.low_freq_factor, c.high_freq_factor = float(low_freq_factor), float(high_freq_factor)
+        c.beta_fast, c.beta_slow = float(beta_fast), float(beta_slow)
+        c.magnitude = float(magnitude)
+        turns = (ctypes.c_uint64 * max(1, min(c.rot_dim, 1 << 10)))()
+        mag = ctypes.c_float()
+        _check(lib().ekv_rope_table(ctypes.byref(c), turns, ctypes.byref(mag)), "ekv_rope_table")
+        self.cfg, self.magnitude = c, mag.value
+        self.turns = list(turns[:c.rot_dim // 2])
+        self.device = torch.device("cuda" if device is None else device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        signed = [t - (1 << 64) if t >= 1 << 63 else t for t in self.turns]
+        self.table = torch.tensor(signed, dtype=torch.int64, device=self.device)
+
+    def __call__(self, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                 stream=None):
+        """(q_out, k_out): q [n, Hq, d] and k [n, Hkv, d] (either may be None) turned to
+        positions [n] int32.  Token strides are free (views of a fused projection),
+        the heads of a token contiguous; q_out / k_out may be q / k (in place)."""
+        d, n, dev = self.cfg.head_dim, positions.numel(), self.device
+        _need("positions", positions, torch.int32, (n,), dev)
+        ins, outs, st_in, st_out = [q, k], [q_out, k_out], [0, 0], [0, 0]
+        for i, name in enumerate("qk"):
+            if ins[i] is None:
+                if outs[i] is not None:
+                    raise ValueError(f"{name}_out without {name}")
+                continue
+            _need(name, ins[i], torch.float16, (n, None, d), dev, contiguous=False)
+            st_in[i] = _token_stride(name, ins[i])
+            if outs[i] is not None:
+                _need(name + "_out", outs[i], torch.float16, tuple(ins[i].shape), dev,
+                      contiguous=False)
+                st_out[i] = _token_stride(name + "_out", outs[i])
+        with _on(dev, stream) as s:
+            for i in range(2):
+                if ins[i] is not None and outs[i] is None:
+                    outs[i] = torch.empty(ins[i].shape, dtype=torch.float16, device=dev)
+                    st_out[i] = _token_stride("out", outs[i])
+            heads = [0 if x is None else x.shape[1] for x in ins]
+            _check(lib().ekv_rope(ctypes.byref(self.cfg), _ptr(self.table), n, _ptr(positions),
+                                  heads[0], _ptr(ins[0]), st_in[0], _ptr(outs[0]), st_out[0],
+                                  heads[1], _ptr(ins[1]), st_in[1], _ptr(outs[1]), st_out[1], s),
+                   "ekv_rope")
+        return outs[0], outs[1]
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                softmax_scale: float = 0.0, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts (ekv_prompt_attn): q [T, Hq, d], k and v
+    [T, Hkv, d] fp16 (token strides free), cu_seqlens [n + 1] int32 row bounds.
+    Rows outside every sequence are not written (a new `out` holds anything there)."""
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
+        raise TypeError("q and k must be tensors")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must have shape [tokens, heads, d]")
+    T, Hq, d = q.shape
+    Hkv, dev = k.shape[1], q.device
+    _need("q", q, torch.float16, (T, Hq, d), dev, contiguous=False)
+    _need("k", k, torch.float16, (T, Hkv, d), dev, contiguous=False)
+    _need("v", v, torch.float16, (T, Hkv, d), dev, contiguous=False)
+    _need("cu_seqlens", cu_seqlens, torch.int32, (None,), dev)
+    if out is not None:
+        _need("out", out, torch.float16, (T, Hq, d), dev, contiguous=False)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold n + 1 bounds")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
+        st = [_token_stride(nm, t) for nm, t in (("q", q), ("k", k), ("v", v), ("out", out))]
+        _check(lib().ekv_prompt_attn(Hq, Hkv, d, float(softmax_scale), T, cu_seqlens.numel() - 1,
+                                     _ptr(cu_seqlens), _ptr(q), st[0], _ptr(k), st[1], _ptr(v),
+                                     st[2], _ptr(out), st[3], s), "ekv_prompt_attn")
+    return out
+
+
+def verify_tree(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
+                u_accept: torch.Tensor, u_sample: torch.Tensor,
+                draft_probs: torch.Tensor | None = None, n_nodes: torch.Tensor | None = None,
+                stream=None):
+    """Verify drafted trees (ekv_verify_tree): target_probs [n, m, V] fp32 (row i: after
+    node i), tokens and parents [n, m] int32, u_accept [n, m] and u_sample [n] fp32 in
+    [0, 1), draft_probs [n, m, V] or None, n_nodes [n] int32 or None.  Returns int32
+    (path [n, m], n_accept [n], next_token [n])."""
+    if not isinstance(target_probs, torch.Tensor):
+        raise TypeError("target_probs must be a tensor")
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must have shape [n, m, V]")
+    n, m, V = target_probs.shape
+    dev = target_probs.device
+    for name, t, dt, shape in (("tokens", tokens, torch.int32, (n, m)),
+                               ("parents", parents, torch.int32, (n, m)),
+                               ("u_accept", u_accept, torch.float32, (n, m)),
+                               ("u_sample", u_sample, torch.float32, (n,))):
+        _need(name, t, dt, shape, dev)
+    if n_nodes is not None:
+        _need("n_nodes", n_nodes, torch.int32, (n,), dev)
+    strides = []
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is None:
+            strides += [0, 0]
+            continue
+        _need(name, t, torch.float32, (n, m, V), dev, contiguous=False)
+        if V > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name}: a row's entries must be contiguous")
+        strides += [t.stride(0) if n > 1 else 0, t.stride(1) if m > 1 else V]
+    with _on(dev, stream) as s:
+        path = torch.empty(n, m, dtype=torch.int32, device=dev)
+        n_accept = torch.empty(n, dtype=torch.int32, device=dev)
+        nxt = torch.empty(n, dtype=torch.int32, device=dev)
+        _check(lib().ekv_verify_tree(n, m, V, _ptr(target_probs), strides[0], strides[1],
+                                     _ptr(draft_probs), strides[2], strides[3], _ptr(tokens),
+                                     _ptr(parents), _ptr(n_nodes), _ptr(u_accept), _ptr(u_sample),
+                                     _ptr(path), _ptr(n_accept), _ptr(nxt), s), "ekv_verify_tree")
+    return path, n_accept, nxt
 
 
 def abs_percentile(x: torch.Tensor, q: float, n_rows: int, row_stride: int, n_groups: int,
