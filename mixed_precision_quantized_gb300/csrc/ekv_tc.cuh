@@ -108,6 +108,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : EKV_R8(r, 0), EKV_R8(r, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      EKV_I8(r, 0), EKV_I8(r, 8)
+      : "memory");
+}
+
 // ---- MMA -------------------------------------------------------------------------
 // Descriptor of an operand in shared memory, 128-byte swizzle.  K-major (rows of the
 // operand are rows of the tile): `sbo` 1024 between groups of 8 rows, `lbo` unused.

@@ -6,103 +6,1011 @@
 // reads them, and over itself and its ancestors among the drafted nodes:
 //   o_ih = sum_{t cached} p_t vhat_t + sum_{a in anc(i)} p_a v_a,
 //   p = softmax over both of sigma q_ih . khat_t and sigma q_ih . k_a.
-// One warp per (node, query head): lanes hold 1/32 of the head's channels, keys are
-// taken one at a time with a running maximum and sum.
+//
+// The rows of one (sequence, KV head) are its nodes times the G query heads of the group
+// (1 to 512), so each page is worth 16 keys to all of them: it is read from memory and
+// unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
+// tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
+//   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
+//   warps 8-15   unpack a raw tile into swizzled fp16 operand tiles: K as hi + lo
+//                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K
+//                need hi alone), V as the bare codes (exact in fp16)
+//   warp 16      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
+//   warps 0-3, 4-7  two softmax streams, one row a thread
+// With more than 128 rows the two streams are two row tiles over the same tokens; with
+// fewer they are the even and odd token tiles of the same rows, merged at the end
+// (each reads the other's accumulator in tensor memory).
+//
+// A token's V scale s multiplies its probability: P' = 2^(x + log2 s - m) in fp16, where
+// the reference m follows the largest x + log2 s, so the fp16 range is used well whatever
+// the scales; the row sum adds P' / s in fp32.  As in prompt attention m moves only for
+// a gain above 2^8, P' carries 2^7, and P' is the one value rounded to fp16.
+//
+// Work split: all (sequence, KV head, row pair) units laid end to end in cost order of
+// their tiles, cut into equal runs, one per CTA (one CTA an SM); a run may hold parts of
+// several units.  A unit cut by run ends leaves fp32 partials (numerator, max, sum) in
+// the scratch, and a second small kernel merges them by log-sum-exp.  The cut depends on
+// the lengths only, so equal calls give equal bits.
 #include <math_constants.h>
 
 #include "ekv_internal.h"
+#include "ekv_tc.cuh"
 
 namespace ekv {
 namespace {
 
-// Value of channel c, row r of a quantized part of b bits (raw fp16 at 16).
-__device__ float code_at(const uint8_t* part, int d, int b, int r, int c, bool asym) {
-  if (b == 16) return __half2float(reinterpret_cast<const __half*>(part)[r * d + c]);
-  const int u = (part[r * (d * b / 8) + c * b / 8] >> ((c * b) % 8)) & ((1 << b) - 1);
-  return (float)(asym ? u : u - (1 << (b - 1)));
+using namespace tc;
+
+constexpr int TM_ROWS = 128;      // rows of a row tile
+constexpr int TN = 64;            // tokens of a token tile
+constexpr int TPAGES = TN / BLOCK;
+constexpr int TT = 640;           // threads
+// 96 registers a thread at launch (65,536 / 640, in eights: 61,440 in all); softmax takes
+// 128, unpacking 80, the rest 56: 256 x 128 + 256 x 80 + 128 x 56 = 60,416.
+constexpr int TREGS_SOFTMAX = 128, TREGS_UNPACK = 80, TREGS_OTHER = 56;
+constexpr int TSEQS = 512;        // sequences of one launch
+constexpr int TSTAGES = 2;        // operand tiles in flight
+constexpr int RAW_BYTES = 96 * 1024;
+constexpr int RAW_MAX = 8;        // raw tiles in flight at most
+constexpr int DW = 8;             // unpacking warps
+
+template <int D>
+struct TCfg {
+  static constexpr int SUBT = TN * 128;              // 64 channels of a tile
+  static constexpr int OPND = D / 64 * SUBT;         // one operand tile
+  static constexpr int STAGE = 3 * OPND;             // K hi, K lo, V
+  static constexpr int RAW_OFF = TSTAGES * STAGE;
+  static constexpr int MISC_OFF = RAW_OFF + RAW_BYTES;
+};
+
+struct TMisc {
+  int64_t pre[TSEQS + 1];       // cost of the sequences before
+  int32_t len[TSEQS];           // cached tokens
+  int32_t slot[TSEQS];
+  uint8_t cnt[TSEQS];           // nodes
+  unsigned long long anc[2][64];  // ancestors-or-self of each node, by segment parity
+  // of each token's V scale s: log2 s, 1 / s and (asymmetric) the zero point over s
+  alignas(16) float lsv[TSTAGES][TN];
+  alignas(16) float rsv[TSTAGES][TN];
+  alignas(16) float zsv[TSTAGES][TN];
+  alignas(8) uint16_t valid[TSTAGES][TPAGES];  // tokens that are there
+  int32_t has_lo[TSTAGES];
+  int32_t ent[RAW_MAX][TPAGES];
+  float ml[2][3][TM_ROWS];      // (m, l, z) of the two streams
+  alignas(8) uint64_t bars[2 * TSTAGES + 2 * RAW_MAX + 4 * 2];
+  int stop;
+  uint32_t tmem;
+};
+
+struct TreeArgs {
+  int layer, vb, m, n_seqs;
+  const int32_t *slots, *n_nodes, *parents;
+  const __half *q, *k, *v;
+  __half* o;
+  float* acc;       // [2 grid][2 row tiles][D / 4][128] float4
+  float2* ml;       // [2 grid][2][128] (max, sum)
+  int64_t* pre;     // [n_seqs + 1] for the merging kernel
+  int grid;
+};
+
+__host__ __device__ inline int rows_of(int cnt, int G) { return cnt * G; }
+__host__ __device__ inline int pairs_of(int rows) {  // row-tile pairs
+  return (rows + 2 * TM_ROWS - 1) / (2 * TM_ROWS);
 }
-// Position of channel c's K scale (pair order of 2- and 4-bit pages).
-__device__ int k_scale_pos(int b, int c) {
-  if (b >= 8) return c;
-  const int n = 32 / b, i = c % n;
-  return c - i + (i < n / 2 ? 2 * i : 2 * (i - n / 2) + 1);
+// Cost of one token tile: two row tiles take about 3/2 of the time of one (the pages
+// and their unpacking are shared).
+__host__ __device__ inline int tile_cost(int rows) { return rows > TM_ROWS ? 3 : 2; }
+__host__ __device__ inline int tiles_of(int len) { return (len + TN - 1) / TN + 1; }  // + drafts
+__host__ __device__ inline int64_t seq_cost(int len, int cnt, int G, int Hkv) {
+  const int r = rows_of(cnt, G);
+  return cnt > 0 ? (int64_t)Hkv * pairs_of(r) * tiles_of(len) * tile_cost(r) : 0;
+}
+__host__ __device__ inline int64_t run_start(int64_t total, int c, int grid) {
+  return total * c / grid;
+}
+// Tiles of a unit at cost offset a that lie in the run [lo, hi).
+__host__ __device__ inline void unit_part(int64_t a, int nt, int cost, int64_t lo, int64_t hi,
+                                          int& s, int& e) {
+  const int64_t x = lo > a ? (lo - a + cost - 1) / cost : 0;
+  const int64_t y = hi > a ? (hi - a + cost - 1) / cost : 0;
+  s = (int)(x < nt ? x : nt);
+  e = (int)(y < nt ? y : nt);
+}
+
+// A CTA's segments in order, the same in every role.
+struct Walk {
+  int64_t lo, hi, a;       // run, cost offset of the unit
+  int z, unit, nunits, nt, cost;
+  int h, row0, nrt, rows, s, e, len, cnt, n;
+  __device__ void init(const TMisc& M, int n_seqs, int grid) {
+    n = n_seqs;
+    const int64_t total = M.pre[n_seqs];
+    lo = run_start(total, blockIdx.x, grid);
+    hi = run_start(total, blockIdx.x + 1, grid);
+    int p = 0, q = n_seqs;  // the last sequence that starts at or before lo
+    while (q - p > 1) {
+      const int mid = (p + q) / 2;
+      if (M.pre[mid] <= lo) p = mid;
+      else q = mid;
+    }
+    z = p - 1;
+    unit = nunits = 0;
+  }
+  __device__ bool next(const TMisc& M, int G, int Hkv) {
+    while (true) {
+      if (unit >= nunits) {
+        if (++z >= n || M.pre[z] >= hi) return false;
+        len = M.len[z];
+        cnt = M.cnt[z];
+        const int r = rows_of(cnt, G);
+        nunits = cnt > 0 ? Hkv * pairs_of(r) : 0;
+        nt = tiles_of(len);
+        cost = tile_cost(r);
+        a = M.pre[z];
+        unit = 0;
+        if (nunits && lo > a) {  // skip the units before the run
+          const int64_t skip = (lo - a) / ((int64_t)nt * cost);
+          unit = (int)(skip < nunits ? skip : nunits);
+          a += (int64_t)unit * nt * cost;
+        }
+        continue;
+      }
+      if (a >= hi) return false;
+      unit_part(a, nt, cost, lo, hi, s, e);
+      const int np = pairs_of(rows_of(cnt, G));
+      h = unit / np;
+      row0 = unit % np * 2 * TM_ROWS;
+      rows = min(2 * TM_ROWS, rows_of(cnt, G) - row0);
+      nrt = rows > TM_ROWS ? 2 : 1;
+      begun_ = a;
+      a += (int64_t)nt * cost;
+      ++unit;
+      if (s < e) return true;
+    }
+  }
+  int64_t begun_;          // cost offset of the segment's unit
+  __device__ bool whole() const { return s == 0 && e == nt; }
+  __device__ int part_slot() const { return 2 * blockIdx.x + (lo > begun_ ? 0 : 1); }
+};
+
+// ---- unpacking: 8 channels (group g) of one row as 4 words, in the order
+// (0,4) (1,5) (2,6) (3,7), which 4-bit words unpack to with one AND-OR a pair.  Q is
+// permuted the same way when it is loaded and O back when it is written. --------------
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hfma(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            *reinterpret_cast<__half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmul(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hneg(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ void perm8(const uint4& u, uint32_t* w) {
+  w[0] = __byte_perm(u.x, u.z, 0x5410);
+  w[1] = __byte_perm(u.x, u.z, 0x7632);
+  w[2] = __byte_perm(u.y, u.w, 0x5410);
+  w[3] = __byte_perm(u.y, u.w, 0x7632);
+}
+
+constexpr uint32_t MAGIC = 0x64006400u;   // fp16 1024, 1024
+// fp16 constants (both halves): 1024 + offset of the code width, and the same over the
+// power of two that a code's position in the word multiplies it by.
+__device__ __forceinline__ constexpr uint32_t both(uint32_t h) { return h | h << 16; }
+
+// Codes of B bits (signed q for the symmetric quantizer, unsigned u for the other), or raw
+// fp16 for B = 16.  `row` points at the row's first byte.
+template <int B, bool ASYM>
+__device__ __forceinline__ void unpack8w(const uint8_t* row, int g, uint32_t* w) {
+  if constexpr (B == 16) {
+    perm8(*reinterpret_cast<const uint4*>(row + 16 * g), w);
+  } else if constexpr (B == 8) {
+    const uint2 r = *reinterpret_cast<const uint2*>(row + 8 * g);
+    const uint32_t y0 = __byte_perm(r.x, r.y, 0x5140), y1 = __byte_perm(r.x, r.y, 0x7362);
+    const uint32_t sub = both(ASYM ? 0x6400 : 0x6480);  // 1024 or 1152
+    w[0] = hsub(__byte_perm(y0, 0x64646464u, 0x4140), sub);
+    w[1] = hsub(__byte_perm(y0, 0x64646464u, 0x4342), sub);
+    w[2] = hsub(__byte_perm(y1, 0x64646464u, 0x4140), sub);
+    w[3] = hsub(__byte_perm(y1, 0x64646464u, 0x4342), sub);
+  } else if constexpr (B == 4) {
+    const uint32_t r = *reinterpret_cast<const uint32_t*>(row + 4 * g), r8 = r >> 8;
+    const uint32_t lo = both(ASYM ? 0x6400 : 0x6408);   // 1024 or 1032
+    const uint32_t hi = both(ASYM ? 0xD400 : 0xD480);   // -64 or -72
+    const uint32_t q16 = both(0x2C00);                  // 1/16
+    w[0] = hsub(and_or(r, 0x000F000Fu, MAGIC), lo);
+    w[1] = hfma(and_or(r, 0x00F000F0u, MAGIC), q16, hi);
+    w[2] = hsub(and_or(r8, 0x000F000Fu, MAGIC), lo);
+    w[3] = hfma(and_or(r8, 0x00F000F0u, MAGIC), q16, hi);
+  } else {
+    const uint32_t r = *reinterpret_cast<const uint16_t*>(row + 2 * g);
+    const uint32_t x = __byte_perm(r, 0, 0x4140);
+    w[0] = hsub(and_or(x, 0x00030003u, MAGIC), both(ASYM ? 0x6400 : 0x6402));
+    w[1] = hfma(and_or(x, 0x000C000Cu, MAGIC), both(0x3400), both(ASYM ? 0xDC00 : 0xDC08));
+    w[2] = hfma(and_or(x, 0x00300030u, MAGIC), both(0x2C00), both(ASYM ? 0xD400 : 0xD420));
+    w[3] = hfma(and_or(x, 0x00C000C0u, MAGIC), both(0x2400), both(ASYM ? 0xCC00 : 0xCC80));
+  }
+}
+// Per-channel fp16 values (scales or zero points) of group g in the same order.
+template <int B>
+__device__ __forceinline__ void channel8(const uint8_t* arr, int g, uint32_t* w) {
+  if constexpr (B == 8) {
+    perm8(*reinterpret_cast<const uint4*>(arr + 16 * g), w);
+  } else if constexpr (B == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(arr + 16 * g);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {  // word j of 16 channels holds channels j and j + 8
+    const uint4 a = *reinterpret_cast<const uint4*>(arr + 32 * (g >> 1));
+    const uint4 b = *reinterpret_cast<const uint4*>(arr + 32 * (g >> 1) + 16);
+    const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+    w[0] = __byte_perm(a.x, b.x, sel);
+    w[1] = __byte_perm(a.y, b.y, sel);
+    w[2] = __byte_perm(a.z, b.z, sel);
+    w[3] = __byte_perm(a.w, b.w, sel);
+  }
 }
 
 template <int D>
-__global__ void __launch_bounds__(128)
-tree_kernel(DevState st, int layer, int vb, int m, const int32_t* __restrict__ slots,
-            const int32_t* __restrict__ n_nodes, const int32_t* __restrict__ parents,
-            const __half* __restrict__ q, const __half* __restrict__ k,
-            const __half* __restrict__ v, __half* __restrict__ o, int n_seqs) {
-  constexpr int C = D / 32;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (int64_t)n_seqs * m * st.Hq) return;
-  const int h = (int)(row % st.Hq), i = (int)(row / st.Hq % m), z = (int)(row / st.Hq / m);
-  const int g = h / st.G, cnt = n_nodes ? min(m, n_nodes[z]) : m;
-  if (i >= cnt) return;
-  const int slot = slots[z];
-  const bool slot_ok = slot >= 0 && slot < st.S;
-  if (!slot_ok && lane == 0) set_error(st, EKV_EINVAL);
-  const int T = slot_ok ? st.len[ls_index(st, layer, slot)] : 0;
-  float qf[C], acc[C], mx = -CUDART_INF_F, l = 0.f;
-  for (int c = 0; c < C; ++c) {
-    qf[c] = __half2float(q[(((size_t)z * m + i) * st.Hq + h) * D + lane * C + c]) * st.scale_log2;
-    acc[c] = 0.f;
+__device__ __forceinline__ uint32_t tile_at(int row, int g) {  // 16-byte chunk of a tile
+  return (g >> 3) * TCfg<D>::SUBT + row * 128 + (((g & 7) ^ (row & 7)) << 4);
+}
+
+// One warp unpacks half of a page's 16 rows (tile rows r0 ..): group g of rows t0, t0 +
+// step, ...; rows from `n` on hold no token (K left as it is, V zero).
+template <int D>
+struct Half {
+  static constexpr int GR = D / 8, LANES = 32 / GR;  // groups, rows side by side
+  int g, t0, step, nrow;
+  __device__ Half(int half, int lane) {
+    g = lane % GR;
+    t0 = half * LANES + lane / GR;
+    step = 2 * LANES;
+    nrow = BLOCK / (2 * LANES);
   }
-  auto add = [&](const float* kf, const float* vf) {
-    float x = 0.f;
-    for (int c = 0; c < C; ++c) x = fmaf(qf[c], kf[c], x);
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    const float mn = fmaxf(mx, x), al = exp2f(mx - mn), p = exp2f(x - mn);
-    l = l * al + p;
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(p, vf[c], acc[c] * al);
-    mx = mn;
-  };
-  const size_t lsh = lsh_index(st, layer, slot_ok ? slot : 0, g);
-  for (int t = 0; t < T; ++t) {
-    const int32_t e = st.bt[lsh * st.maxblk + t / BLOCK];
-    if (e == -1) {
-      if (lane == 0) set_error(st, EKV_ESTATE);
-      continue;
+};
+
+template <int D, int KB, bool ASYM>
+__device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int n, uint8_t* hi,
+                                         uint8_t* lo, bool want_lo, int r0, const Half<D>& hf) {
+  uint32_t sc[4], zp[4];
+  if constexpr (KB < 16) {
+    channel8<KB>(kp + BLOCK * D * KB / 8, hf.g, sc);
+    if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, hf.g, zp);
+  }
+#pragma unroll
+  for (int i = 0; i < 16 / (2 * Half<D>::LANES); ++i) {
+    const int t = hf.t0 + i * hf.step;
+    if (t >= n) break;
+    uint32_t w[4], l[4] = {0, 0, 0, 0};
+    unpack8w<KB, ASYM>(kp + t * stride, hf.g, w);
+    if constexpr (KB < 16 && !ASYM) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t p = hmul(w[j], sc[j]);
+        if constexpr (KB > 2) l[j] = hfma(w[j], sc[j], hneg(p));  // exact residual
+        w[j] = p;
+      }
+    } else if constexpr (KB < 16) {  // u s + z in fp32, then hi + lo
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = __half22float2(*reinterpret_cast<__half2*>(&w[j]));
+        const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[j]));
+        const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[j]));
+        const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
+        const __half2 p = __floats2half2_rn(a, b);
+        const float2 pf = __half22float2(p);
+        const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
+        w[j] = *reinterpret_cast<const uint32_t*>(&p);
+        l[j] = *reinterpret_cast<const uint32_t*>(&r);
+      }
     }
-    const int fmt = entry_fmt(e), kb = bits_of_code(fmt >> 2), r = t % BLOCK;
-    const bool asym = st.asym != 0, open = t / BLOCK * BLOCK + BLOCK > T;
-    const uint8_t* kp = st.pool_base[fmt] + (size_t)entry_idx(e) * st.pool_page_bytes[fmt];
-    const uint8_t* vp = kp + k_part_bytes(kb, D, asym);
-    const __half* ks = reinterpret_cast<const __half*>(kp + BLOCK * D * kb / 8);
-    const __half* vs = reinterpret_cast<const __half*>(vp + BLOCK * D * vb / 8);
-    float kf[C], vf[C];
-    for (int c = 0; c < C; ++c) {
-      const int ch = lane * C + c;
-      if (open) {
-        kf[c] = __half2float(st.staging[lsh * (BLOCK * D) + r * D + ch]);
-      } else {
-        kf[c] = code_at(kp, D, kb, r, ch, asym);
-        if (kb < 16) {
-          const int sp = k_scale_pos(kb, ch);
-          kf[c] = kf[c] * __half2float(ks[sp]) + (asym ? __half2float(ks[D + sp]) : 0.f);
+    const uint32_t at = tile_at<D>(r0 + t, hf.g);
+    *reinterpret_cast<uint4*>(hi + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (want_lo) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+// V codes are signed for both quantizers: u s + z = (u - 2^(b-1)) s + (z + 2^(b-1) s), so
+// that the products P' q stay as small as the values.
+template <int D, int VB>
+__device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int n, uint8_t* dst,
+                                         int r0, const Half<D>& hf) {
+#pragma unroll
+  for (int i = 0; i < 16 / (2 * Half<D>::LANES); ++i) {
+    const int t = hf.t0 + i * hf.step;
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (t < n) unpack8w<VB, false>(vp + t * stride, hf.g, w);
+    *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int D, bool ASYM>
+__global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
+  using Cfg = TCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  TMisc& M = *reinterpret_cast<TMisc*>(smem + Cfg::MISC_OFF);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t b0 = smem_u32(M.bars);
+  const uint32_t tile_full = b0, tile_empty = b0 + 8 * TSTAGES, raw_full = tile_empty + 8 * TSTAGES,
+                 raw_empty = raw_full + 8 * RAW_MAX, q_full = raw_empty + 8 * RAW_MAX,
+                 s_full = q_full + 16, p_full = s_full + 16, o_done = p_full + 16;
+  volatile int* stop = &M.stop;
+
+  for (int z = tid; z < A.n_seqs; z += TT) {
+    const int slot = A.slots[z];
+    const bool ok = slot >= 0 && slot < st.S;
+    if (!ok && blockIdx.x == 0) set_error(st, EKV_EINVAL);
+    const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
+    M.slot[z] = ok ? slot : 0;
+    M.len[z] = ok ? st.len[ls_index(st, A.layer, slot)] : 0;
+    M.cnt[z] = (uint8_t)cnt;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < TSTAGES; ++i) {
+      bar_init(tile_full + 8 * i, DW);
+      bar_init(tile_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < RAW_MAX; ++i) {
+      bar_init(raw_full + 8 * i, 1);
+      bar_init(raw_empty + 8 * i, DW);
+    }
+    for (int t = 0; t < 2; ++t) {
+      bar_init(q_full + 8 * t, 4);
+      bar_init(s_full + 8 * t, 1);
+      bar_init(p_full + 8 * t, 4);
+      bar_init(o_done + 8 * t, 1);
+    }
+    M.stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 16) tmem_alloc(smem_u32(&M.tmem), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = M.tmem;  // stream t at 256 t: Q (D / 2 columns), S and P at 64, O at 128
+  if (warp == 0) {             // prefix of the sequences' costs
+    int64_t run = 0;
+    for (int z0 = 0; z0 < A.n_seqs; z0 += 32) {
+      const int z = z0 + lane;
+      const int64_t c = z < A.n_seqs ? seq_cost(M.len[z], M.cnt[z], st.G, st.Hkv) : 0;
+      int64_t x = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      if (z < A.n_seqs) M.pre[z] = run + x - c;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) M.pre[A.n_seqs] = run;
+    __syncwarp();
+    if (blockIdx.x == 0)
+      for (int z = lane; z <= A.n_seqs; z += 32) A.pre[z] = M.pre[z];
+  }
+  __syncthreads();
+
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_OTHER));
+    Walk w;
+    w.init(M, A.n_seqs, A.grid);
+    // Raw tile: 4 pages, each sized for the widest page the layer has admitted.
+    const int kmax = max(2, st.kmax[A.layer]);
+    const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
+    const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
+    if (warp == 17) {
+      // ---- page copies ---------------------------------------------------------------
+      int rs = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      while (ok && w.next(M, st.G, st.Hkv)) {
+        const int32_t* bt = st.bt + lsh_index(st, A.layer, M.slot[w.z], w.h) * st.maxblk;
+        const int nblk = (w.len + BLOCK - 1) / BLOCK, sealed = w.len / BLOCK;
+        const int end = min(w.e, w.nt - 1);  // the drafts' tile has no pages
+        int32_t ahead = -1;
+        for (int i = w.s; i < end && ok; ++i) {
+          const int k = (i - w.s) & 7;
+          if (k == 0) {  // table entries of the next 8 tiles
+            const int b = i * TPAGES + lane;
+            ahead = b < nblk ? bt[b] : -1;
+          }
+          ok = bar_wait(raw_empty + 8 * rs, ph, stop);
+          if (!ok) break;
+          const int32_t e = __shfl_sync(0xffffffffu, ahead, k * TPAGES + (lane & 3));
+          const int b = i * TPAGES + (lane & 3);
+          uint32_t bytes = 0;
+          if (lane < TPAGES && b < nblk) {
+            if (e == -1) set_error(st, EKV_ESTATE);
+            else if (b < sealed) bytes = (uint32_t)st.pool_page_bytes[entry_fmt(e)];
+          }
+          if (lane < TPAGES) M.ent[rs][lane] = b < nblk ? e : -1;
+          uint32_t all = bytes;
+          all += __shfl_xor_sync(0xffffffffu, all, 1);
+          all += __shfl_xor_sync(0xffffffffu, all, 2);
+          __syncwarp();
+          if (lane == 0) bar_expect(raw_full + 8 * rs, all);
+          __syncwarp();
+          if (bytes) {
+            const int fmt = entry_fmt(e);
+            const uint8_t* src = st.pool_base[fmt] + (size_t)entry_idx(e) * bytes;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
+                "%2, [%3];" ::"r"(sb + Cfg::RAW_OFF + (rs * TPAGES + lane) * page_room),
+                "l"(src), "r"(bytes), "r"(raw_full + 8 * rs)
+                : "memory");
+          }
+          if (++rs == nraw) {
+            rs = 0;
+            ph ^= 1;
+          }
         }
       }
-      vf[c] = code_at(vp, D, vb, r, ch, asym);
-      if (vb < 16)
-        vf[c] = vf[c] * __half2float(vs[r]) + (asym ? __half2float(vs[BLOCK + r]) : 0.f);
+    } else if (warp == 16) {
+      // ---- products ------------------------------------------------------------------
+      constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false), ID_O = idesc_f16(TM_ROWS, D, true);
+      int stage = 0;
+      uint32_t fph = 0, qph = 0, pph = 0;
+      bool ok = true;
+      auto scores = [&](int t, int sg) {
+        const uint32_t base = sb + sg * Cfg::STAGE, d = tm + 256 * t + 64, q = tm + 256 * t;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ts(d, q + 8 * k,
+                   desc_sw128(base + (k / 4) * Cfg::SUBT + (k % 4) * 32, 16, 1024), ID_S, k > 0);
+          if (M.has_lo[sg]) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ts(d, q + 8 * k,
+                     desc_sw128(base + Cfg::OPND + (k / 4) * Cfg::SUBT + (k % 4) * 32, 16, 1024),
+                     ID_S, true);
+          }
+          mma_commit(s_full + 8 * t);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int t, int sg, bool first) {
+        const uint32_t base = sb + sg * Cfg::STAGE + 2 * Cfg::OPND;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < TN / 16; ++k)
+            mma_ts(tm + 256 * t + 128, tm + 256 * t + 64 + 8 * k,
+                   desc_sw128(base + k * 2048, Cfg::SUBT, 1024), ID_O, !first || k > 0);
+          mma_commit(o_done + 8 * t);
+        }
+        __syncwarp();
+      };
+      auto wait_tile = [&]() {  // the next operand tile; returns its stage
+        ok = ok && bar_wait(tile_full + 8 * stage, fph, stop);
+        const int sg = stage;
+        if (++stage == TSTAGES) {
+          stage = 0;
+          fph ^= 1;
+        }
+        return sg;
+      };
+      auto wait_on = [&](uint32_t bar, uint32_t& bits, int t) {
+        ok = ok && bar_wait(bar + 8 * t, (bits >> t) & 1, stop);
+        bits ^= 1u << t;
+        fence_after();
+      };
+      while (ok && w.next(M, st.G, st.Hkv)) {
+        const int n = w.e - w.s;
+        if (w.nrt == 2) {
+          int sg = wait_tile();
+          for (int t = 0; t < 2; ++t) {
+            wait_on(q_full, qph, t);
+            if (ok) scores(t, sg);
+          }
+          for (int i = 0; i < n && ok; ++i) {
+            const int nx = i + 1 < n ? wait_tile() : 0;
+            for (int t = 0; t < 2 && ok; ++t) {
+              wait_on(p_full, pph, t);
+              if (!ok) break;
+              values(t, sg, i == 0);
+              if (i + 1 < n) scores(t, nx);
+            }
+            if (ok && lane == 0) mma_commit(tile_empty + 8 * sg);
+            sg = nx;
+          }
+        } else {
+          wait_on(q_full, qph, 0);
+          wait_on(q_full, qph, 1);
+          int sg = wait_tile();
+          if (ok) scores(0, sg);
+          for (int i = 0; i < n && ok; ++i) {
+            const int t = i & 1;
+            int nx = 0;
+            if (i + 1 < n) {
+              nx = wait_tile();
+              fence_after();
+              if (ok) scores(t ^ 1, nx);
+            }
+            wait_on(p_full, pph, t);
+            if (!ok) break;
+            values(t, sg, i < 2);
+            if (lane == 0) mma_commit(tile_empty + 8 * sg);
+            sg = nx;
+          }
+        }
+      }
     }
-    add(kf, vf);
-  }
-  for (int a = i, steps = 0; a >= 0 && steps < m; ++steps) {
-    float kf[C], vf[C];
-    for (int c = 0; c < C; ++c) {
-      const size_t at = (((size_t)z * m + a) * st.Hkv + g) * D + lane * C + c;
-      kf[c] = __half2float(k[at]);
-      vf[c] = __half2float(v[at]);
+  } else if (warp >= 8) {
+    // ---- unpacking -------------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_UNPACK));
+    Walk w;
+    w.init(M, A.n_seqs, A.grid);
+    const int kmax = max(2, st.kmax[A.layer]);
+    const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
+    const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
+    const int pg = (warp - 8) >> 1;  // page of the tile
+    const Half<D> hf(warp & 1, lane);
+    int rs = 0, stage = 0;
+    uint32_t rph = 0, eph = 1;
+    bool ok = true;
+    while (ok && w.next(M, st.G, st.Hkv)) {
+      const __half* stg = st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
+      for (int i = w.s; i < w.e && ok; ++i) {
+        const bool drafts = i == w.nt - 1;
+        if (!drafts) ok = bar_wait(raw_full + 8 * rs, rph, stop);
+        ok = ok && bar_wait(tile_empty + 8 * stage, eph, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* hi = smem + stage * Cfg::STAGE;
+        uint8_t* lo = hi + Cfg::OPND;
+        uint8_t* vt = lo + Cfg::OPND;
+        const int blk = i * TPAGES + pg;
+        // where the page's rows are, how many hold tokens, and whether the tile needs lo
+        int kb = 16, vb = A.vb, n = 0;
+        bool want_lo = false;
+        const uint8_t *kp = nullptr, *vp = nullptr;
+        int64_t ks, vs;
+        if (drafts) {
+          n = min(BLOCK, max(0, w.cnt - BLOCK * pg));
+          const size_t at = (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
+          kp = reinterpret_cast<const uint8_t*>(A.k + at);
+          vp = reinterpret_cast<const uint8_t*>(A.v + at);
+          vb = 16;
+          ks = vs = (int64_t)st.Hkv * D * 2;
+        } else {
+          for (int x = 0; x < TPAGES; ++x) {
+            const int32_t e = M.ent[rs][x];
+            const int b = bits_of_code(entry_fmt(e) >> 2);
+            if (e != -1 && (i * TPAGES + x + 1) * BLOCK <= w.len)
+              want_lo |= b < 16 && (ASYM || b > 2);
+          }
+          const int32_t e = M.ent[rs][pg];
+          n = e == -1 ? 0 : min(BLOCK, w.len - blk * BLOCK);
+          if (n > 0) {
+            const int fmt = entry_fmt(e);
+            const int pkb = bits_of_code(fmt >> 2);
+            kp = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
+            vp = kp + k_part_bytes(pkb, D, ASYM);
+            if (n == BLOCK) {
+              kb = pkb;
+            } else {  // the open block: raw K rows, V in the page, both read from memory
+              kp = reinterpret_cast<const uint8_t*>(stg);
+              vp = st.pool_base[fmt] + (size_t)entry_idx(e) * st.pool_page_bytes[fmt] +
+                   k_part_bytes(pkb, D, ASYM);
+            }
+          }
+          ks = D * kb / 8;
+          vs = D * vb / 8;
+        }
+        const int r0 = pg * BLOCK;
+        switch (kb) {
+          case 2: unpack_k<D, 2, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
+          case 4: unpack_k<D, 4, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
+          case 8: unpack_k<D, 8, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
+          default: unpack_k<D, 16, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
+        }
+        switch (vb) {
+          case 2: unpack_v<D, 2>(vp, vs, n, vt, r0, hf); break;
+          case 4: unpack_v<D, 4>(vp, vs, n, vt, r0, hf); break;
+          case 8: unpack_v<D, 8>(vp, vs, n, vt, r0, hf); break;
+          default: unpack_v<D, 16>(vp, vs, n, vt, r0, hf); break;
+        }
+        if (!(warp & 1)) {
+          if (lane < BLOCK) {  // scale of token `lane` (rows of scale 0 hold zero codes only)
+            float s = 1.f, zv = 0.f;
+            if (vb < 16 && lane < n) {
+              const __half* sp = reinterpret_cast<const __half*>(vp + BLOCK * D * vb / 8);
+              s = __half2float(sp[lane]);
+              if (ASYM) zv = fmaf(s, (float)(1 << (vb - 1)), __half2float(sp[BLOCK + lane]));
+              if (s == 0.f) s = 1.f;
+            }
+            M.lsv[stage][r0 + lane] = log2f(s);
+            M.rsv[stage][r0 + lane] = 1.f / s;
+            if (ASYM) M.zsv[stage][r0 + lane] = zv / s;
+          }
+          if (lane == 0) {
+            M.valid[stage][pg] = (uint16_t)((1u << n) - 1);
+            if (pg == 0) M.has_lo[stage] = want_lo;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(tile_full + 8 * stage);
+          if (!drafts) bar_arrive(raw_empty + 8 * rs);
+        }
+        if (++stage == TSTAGES) {
+          stage = 0;
+          eph ^= 1;
+        }
+        if (!drafts && ++rs == nraw) {
+          rs = 0;
+          rph ^= 1;
+        }
+      }
     }
-    add(kf, vf);
-    const int up = parents[(size_t)z * m + a];
-    a = up < a ? up : -1;
+  } else {
+    // ---- softmax: thread = row ---------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TREGS_SOFTMAX));
+    Walk w;
+    w.init(M, A.n_seqs, A.grid);
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t base = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tq = base + 256 * t, ts = tq + 64, to = tq + 128;
+    uint32_t sph = 0, oph = 0;
+    int par = 0, tiles_before = 0;  // segment parity; tiles of the segments before
+    bool ok = true;
+    constexpr float SLACK = 8.f, BOOST = 7.f, NONE = -1e30f;
+    while (w.next(M, st.G, st.Hkv)) {
+      // This thread's row: node and query head of the group.
+      const bool split = w.nrt == 1;  // streams share the rows and halve the tiles
+      const int r = w.row0 + (split ? row : t * TM_ROWS + row);
+      const bool mine = r < rows_of(w.cnt, st.G);
+      const int node = mine ? r / st.G : 0, gh = r - node * st.G;
+      const size_t qrow = (((size_t)w.z * A.m + node) * st.Hq + w.h * st.G + (mine ? gh : 0)) * D;
+      const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without rows
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 v = mine ? __ldg(reinterpret_cast<const uint4*>(A.q + qrow) + 8 * c + u)
+                               : make_uint4(0, 0, 0, 0);
+          perm8(v, x + 4 * u);
+        }
+        tmem_st32(tq + 32 * c, x);
+      }
+      tmem_wait_st();
+      fence_before();
+      // Ancestors of the nodes, one warp: pointer doubling over the parents.
+      if (w.e == w.nt && (warp & 3) == 0 && t == 0) {
+        for (int i = lane; i < 64; i += 32) {
+          unsigned long long a = 0;
+          if (i < w.cnt) {
+            int x = i;
+            while (x >= 0) {
+              a |= 1ull << x;
+              const int up = A.parents[(size_t)w.z * A.m + x];
+              x = up < x ? up : -1;
+            }
+          }
+          M.anc[par][i] = a;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(q_full + 8 * t);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // both streams: anc is there
+
+      float mref = NONE;
+      uint64_t l2 = pack2(0.f, 0.f), z2 = pack2(0.f, 0.f);
+      int done = 0;
+      for (int i = split ? w.s + t : w.s; i < w.e; i += split ? 2 : 1) {
+        // The operand stage of a tile: stages go round over all of the CTA's tiles.
+        ok = ok && __all_sync(0xffffffffu, bar_wait(s_full + 8 * t, sph, stop));
+        if (!ok) break;
+        sph ^= 1;
+        fence_after();
+        const int sg = (tiles_before + (i - w.s)) % TSTAGES;
+        if (!idle) {
+          uint32_t s[64];
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          const unsigned long long seen =
+              *reinterpret_cast<const unsigned long long*>(M.valid[sg]) &
+              (i == w.nt - 1 ? M.anc[par][node] : ~0ull);
+          tmem_wait_ld();
+          const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
+          uint64_t y[32];
+          const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const ulonglong2 a = lv[c];
+            const float* x = reinterpret_cast<const float*>(s) + 4 * c;
+            y[2 * c] = fma2(pack2(x[0], x[1]), sl2, a.x);
+            y[2 * c + 1] = fma2(pack2(x[2], x[3]), sl2, a.y);
+          }
+          if (__any_sync(0xffffffffu, seen != ~0ull)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float a, b;
+              unpack2(y[c], a, b);
+              if (!(seen >> (2 * c) & 1)) a = -CUDART_INF_F;
+              if (!(seen >> (2 * c + 1) & 1)) b = -CUDART_INF_F;
+              y[c] = pack2(a, b);
+            }
+          }
+          float mx = -CUDART_INF_F, my = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float a, b;
+            unpack2(y[c], a, b);
+            mx = fmaxf(mx, a);
+            my = fmaxf(my, b);
+          }
+          mx = fmaxf(mx, my);
+          const bool move = mx > mref + SLACK;
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? ex2(mref - mx) : 1.f;
+            if (move) mref = mx;
+            if (done > 0) {  // O holds this stream's products up to the tile before
+              ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+              if (!ok) break;
+              fence_after();
+              l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
+              if (ASYM) z2 = fma2(z2, pack2(f, f), pack2(0.f, 0.f));
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t x[16];
+                tmem_ld16(to + 16 * c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * f);
+                tmem_st16(to + 16 * c, x);
+              }
+            }
+          }
+          const uint64_t off = pack2(BOOST - mref, BOOST - mref);
+          const ulonglong2* rv = reinterpret_cast<const ulonglong2*>(M.rsv[sg]);
+          const ulonglong2* zv = reinterpret_cast<const ulonglong2*>(M.zsv[sg]);
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const ulonglong2 ra = rv[c];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float a, b;
+              unpack2(add2(y[2 * c + u], off), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              const uint64_t ab = pack2(a, b);
+              l2 = fma2(ab, u ? ra.y : ra.x, l2);
+              if (ASYM) {
+                const ulonglong2 za = zv[c];
+                z2 = fma2(ab, u ? za.y : za.x, z2);
+              }
+              const __half2 hh = __floats2half2_rn(a, b);
+              p[2 * c + u] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+          }
+          tmem_st32(ts, p);
+          tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full + 8 * t);
+        oph ^= 1;
+        ++done;
+      }
+      if (ok && done) ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+      fence_after();
+      float la, lb, za, zb;
+      unpack2(l2, la, lb);
+      unpack2(z2, za, zb);
+      float l = la + lb, zs = za + zb, m = mref, f0 = 1.f, f1 = 0.f;
+      int c0 = 0, c1 = D;  // the columns this thread writes
+      float z0 = zs, z1 = 0.f;
+      if (split) {  // the other stream's share of the row; each writes half the columns
+        M.ml[t][0][row] = m;
+        M.ml[t][1][row] = l;
+        M.ml[t][2][row] = zs;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float m0 = M.ml[0][0][row], m1 = M.ml[1][0][row];
+        const float l0 = M.ml[0][1][row], l1 = M.ml[1][1][row];
+        m = fmaxf(m0, m1);
+        f0 = ex2(m0 - m);
+        f1 = ex2(m1 - m);
+        l = f0 * l0 + f1 * l1;
+        z0 = M.ml[0][2][row];
+        z1 = M.ml[1][2][row];
+        c0 = t * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      const bool second = split && w.e - w.s > 1;  // the other stream had a tile
+      const uint32_t oa = split ? base + 128 : to, ob = base + 256 + 128;
+      const float add = f0 * z0 + f1 * z1;
+      const bool direct = w.whole();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int rt = split ? 0 : t;
+      float4* part = reinterpret_cast<float4*>(A.acc) +
+                     ((size_t)w.part_slot() * 2 + rt) * (D / 4) * TM_ROWS;
+      if (!direct && mine && c0 == 0)
+        A.ml[((size_t)w.part_slot() * 2 + rt) * TM_ROWS + row] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 16) {
+        uint32_t x[16], x1[16];
+        tmem_ld16(oa + c, x);
+        if (second) tmem_ld16(ob + c, x1);
+        tmem_wait_ld();
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          // natural channel u of the 16: position in the unpacked order
+          const int at = (u & 8) + ((u & 4) ? 2 * (u & 3) + 1 : 2 * (u & 3));
+          v[u] = f0 * __uint_as_float(x[at]) + add;
+          if (second) v[u] = fmaf(f1, __uint_as_float(x1[at]), v[u]);
+        }
+        if (!mine) continue;
+        if (direct) {
+          uint32_t hw[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const __half2 hh = l > 0.f ? __floats2half2_rn(v[2 * u] * inv, v[2 * u + 1] * inv)
+                                       : __floats2half2_rn(0.f, 0.f);
+            hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(A.o + qrow + c);
+          dst[0] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          dst[1] = make_uint4(hw[4], hw[5], hw[6], hw[7]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            part[(size_t)(c / 4 + u) * TM_ROWS + row] =
+                make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        }
+      }
+      fence_before();
+      if (split) asm volatile("bar.sync 1, 256;" ::: "memory");  // both accumulators are read
+      tiles_before += w.e - w.s;
+      par ^= 1;
+    }
+    if (!ok && lane == 0) set_error(st, EKV_ETIMEOUT);
   }
-  for (int c = 0; c < C; ++c)
-    o[(((size_t)z * m + i) * st.Hq + h) * D + lane * C + c] = __float2half_rn(acc[c] / l);
+  __syncthreads();
+  if (warp == 16) {
+    fence_after();
+    if (*stop) {
+      if (lane == 0) set_error(st, EKV_ETIMEOUT);
+      for (int i = 0; i < 2000; ++i) __nanosleep(1000);  // copies and products in flight land
+    }
+    tmem_free(tm, 512);
+  }
+}
+
+// Merge the partials of the units that run ends cut: a thread per (row, 4 channels).
+template <int D>
+__global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeArgs A, int rt_max,
+                                                             int groups) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int s_slot[256];
+  const int rt = blockIdx.x % rt_max, h = blockIdx.x / rt_max % st.Hkv;
+  const int z = blockIdx.x / rt_max / st.Hkv, row = threadIdx.x;
+  const int slot = A.slots[z];
+  const bool slot_ok = slot >= 0 && slot < st.S;
+  const int len = slot_ok ? st.len[ls_index(st, A.layer, slot)] : 0;
+  const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
+  const int rows = rows_of(cnt, st.G);
+  if (rt * TM_ROWS >= rows) return;
+  const int nt = tiles_of(len), cost = tile_cost(rows);
+  const int64_t total = A.pre[A.n_seqs];
+  const int64_t a = A.pre[z] + (int64_t)(h * pairs_of(rows) + rt / 2) * nt * cost;
+  const int64_t b = a + (int64_t)nt * cost;
+  int c0 = (int)(a * A.grid / total);  // the run that holds a
+  while (c0 > 0 && run_start(total, c0, A.grid) > a) --c0;
+  while (run_start(total, c0 + 1, A.grid) <= a) ++c0;
+  int n = 1;
+  while (c0 + n < A.grid && run_start(total, c0 + n, A.grid) < b) ++n;
+  if (n == 1) return;  // one CTA had the whole unit and wrote o
+  for (int i = row; i < n; i += TM_ROWS) {
+    int s, e;
+    const int64_t lo = run_start(total, c0 + i, A.grid);
+    unit_part(a, nt, cost, lo, run_start(total, c0 + i + 1, A.grid), s, e);
+    s_slot[i] = s == 0 && e == nt ? -2 : s < e ? 2 * (c0 + i) + (lo > a ? 0 : 1) : -1;
+  }
+  __syncthreads();
+  const int r = rt * TM_ROWS + row;
+  if (r >= rows) return;
+  float m = -1e30f;
+  for (int i = 0; i < n; ++i) {
+    if (s_slot[i] == -2) return;
+    if (s_slot[i] >= 0) m = fmaxf(m, A.ml[((size_t)s_slot[i] * 2 + (rt & 1)) * TM_ROWS + row].x);
+  }
+  const int node = r / st.G, gh = r - node * st.G;
+  __half* dst = A.o + (((size_t)z * A.m + node) * st.Hq + h * st.G + gh) * D;
+  for (int g = blockIdx.y * groups; g < (int)(blockIdx.y + 1) * groups; ++g) {
+    float l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      if (s_slot[i] < 0) continue;
+      const size_t at = (size_t)s_slot[i] * 2 + (rt & 1);
+      const float2 ml = A.ml[at * TM_ROWS + row];
+      const float4 x = reinterpret_cast<const float4*>(A.acc)[(at * (D / 4) + g) * TM_ROWS + row];
+      const float f = ex2(ml.x - m);
+      l = fmaf(f, ml.y, l);
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    __align__(8) __half2 hh[2] = {__floats2half2_rn(v.x * inv, v.y * inv),
+                                  __floats2half2_rn(v.z * inv, v.w * inv)};
+    *reinterpret_cast<uint2*>(dst + 4 * g) = *reinterpret_cast<const uint2*>(hh);
+  }
+}
+
+template <int D>
+constexpr int tree_smem() {
+  return TCfg<D>::MISC_OFF + (int)sizeof(TMisc) + 1024;
+}
+
+template <int D, bool ASYM>
+cudaError_t launch_tree(const DevState& st, TreeArgs A, int n_seqs, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(
+      tree_kernel<D, ASYM>, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem<D>());
+  const TreeArgs B = A;
+  for (int z = 0; z < n_seqs && e == cudaSuccess; z += TSEQS) {
+    A.n_seqs = n_seqs - z < TSEQS ? n_seqs - z : TSEQS;
+    A.slots = B.slots + z;
+    A.n_nodes = B.n_nodes ? B.n_nodes + z : nullptr;
+    A.parents = B.parents + (size_t)z * B.m;
+    A.q = B.q + (size_t)z * B.m * st.Hq * D;
+    A.o = B.o + (size_t)z * B.m * st.Hq * D;
+    A.k = B.k + (size_t)z * B.m * st.Hkv * D;
+    A.v = B.v + (size_t)z * B.m * st.Hkv * D;
+    tree_kernel<D, ASYM><<<A.grid, TT, tree_smem<D>(), s>>>(st, A);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) break;
+    // One thread a row and 4 channels; with many row tiles each thread takes 4 of them.
+    const int rt_max = (rows_of(B.m, st.G) + TM_ROWS - 1) / TM_ROWS;
+    const int tiles = A.n_seqs * st.Hkv * rt_max, groups = tiles >= 64 ? 4 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles, D / 4 / groups);
+    cfg.blockDim = dim3(TM_ROWS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, st, A, rt_max, groups);
+  }
+  return e;
+}
+
+struct TreeScratch {
+  int grid = 0;
+  size_t acc = 0, ml = 0, pre = 0, bytes = 0;
+};
+// One CTA an SM; two partials a CTA (its first and its last segment) of two row tiles.
+int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&t->grid, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return EKV_ECUDA;
+  }
+  if (t->grid > 256) t->grid = 256;  // the merging kernel's table of parts
+  const size_t parts = (size_t)t->grid * 2 * 2 * TM_ROWS;
+  const int n = n_seqs < TSEQS ? n_seqs : TSEQS;
+  t->acc = 0;
+  t->ml = parts * st.D * sizeof(float);
+  t->pre = t->ml + parts * sizeof(float2);
+  t->bytes = t->pre + (size_t)(n + 1) * sizeof(int64_t);
+  return EKV_OK;
 }
 
 }  // namespace
@@ -114,8 +1022,11 @@ extern "C" EKV_API int ekv_tree_attn_scratch_bytes(ekv_cache* cache, int32_t n_s
   DevState st;
   int splits, vb, pack;
   if (!out || max_nodes < 1 || max_nodes > EKV_TREE_MAX_NODES) return EKV_EINVAL;
-  const int rc = attn_plan(cache, 0, n_seqs, &st, &splits, &vb, &pack);
-  if (rc == EKV_OK) *out = 0;
+  int rc = attn_plan(cache, 0, n_seqs, &st, &splits, &vb, &pack);
+  if (rc != EKV_OK) return rc;
+  TreeScratch t;
+  rc = tree_scratch(st, n_seqs, &t);
+  if (rc == EKV_OK) *out = (int64_t)t.bytes;
   return rc;
 }
 
@@ -128,20 +1039,35 @@ extern "C" EKV_API int ekv_tree_attn(ekv_cache* cache, int32_t layer, int32_t n_
   DevState st;
   int splits, vb, pack;
   if (max_nodes < 1 || max_nodes > EKV_TREE_MAX_NODES) return EKV_EINVAL;
-  const int rc = attn_plan(cache, layer, n_seqs, &st, &splits, &vb, &pack);
+  int rc = attn_plan(cache, layer, n_seqs, &st, &splits, &vb, &pack);
   if (rc != EKV_OK) return rc;
   if (n_seqs == 0) return EKV_OK;
   if (!seq_slots || !parents || !q || !k || !v || !o) return EKV_EINVAL;
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o) & 15) return EKV_EINVAL;
   if (((uintptr_t)seq_slots | (uintptr_t)n_nodes | (uintptr_t)parents) & 3) return EKV_EINVAL;
-  int64_t need = 0;
-  ekv_tree_attn_scratch_bytes(cache, n_seqs, max_nodes, &need);
-  if (scratch_bytes < need || (need > 0 && (!scratch || ((uintptr_t)scratch & 15))))
-    return EKV_EINVAL;
-  const unsigned grid = (unsigned)(((int64_t)n_seqs * max_nodes * st.Hq + 3) / 4);
-  auto fn = st.D == 64 ? tree_kernel<64> : tree_kernel<128>;
-  fn<<<grid, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      st, layer, vb, max_nodes, seq_slots, n_nodes, parents, static_cast<const __half*>(q),
-      static_cast<const __half*>(k), static_cast<const __half*>(v), static_cast<__half*>(o), n_seqs);
-  return cudaGetLastError() == cudaSuccess ? EKV_OK : EKV_ECUDA;
+  TreeScratch t;
+  rc = tree_scratch(st, n_seqs, &t);
+  if (rc != EKV_OK) return rc;
+  if (!scratch || ((uintptr_t)scratch & 15) || scratch_bytes < (int64_t)t.bytes) return EKV_EINVAL;
+  TreeArgs A = {};
+  A.layer = layer;
+  A.vb = vb;
+  A.m = max_nodes;
+  A.slots = seq_slots;
+  A.n_nodes = n_nodes;
+  A.parents = parents;
+  A.q = static_cast<const __half*>(q);
+  A.k = static_cast<const __half*>(k);
+  A.v = static_cast<const __half*>(v);
+  A.o = static_cast<__half*>(o);
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  A.acc = reinterpret_cast<float*>(base + t.acc);
+  A.ml = reinterpret_cast<float2*>(base + t.ml);
+  A.pre = reinterpret_cast<int64_t*>(base + t.pre);
+  A.grid = t.grid;
+  using Fn = cudaError_t (*)(const DevState&, TreeArgs, int, cudaStream_t);
+  const Fn fn = st.D == 64 ? (st.asym ? launch_tree<64, true> : launch_tree<64, false>)
+                           : (st.asym ? launch_tree<128, true> : launch_tree<128, false>);
+  const cudaError_t e = fn(st, A, n_seqs, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EKV_OK : EKV_ECUDA;
 }

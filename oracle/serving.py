@@ -46,12 +46,14 @@ def rope(x, pos, freqs, mag: float, layout: str) -> np.ndarray:
     return y
 
 
-def attention(q, k, v, see, scale: float | None = None):
+def attention(q, k, v, see, scale: float | None = None, rounded=None):
     """q [n, Hq, d], k and v [T, Hkv, d], see [n, T] truth -> (o [n, Hq, d], bound).
 
     `bound` is how far a kernel may be that rounds each probability (times its value
     row's scale) and the output to fp16 once (2^-11 each) and works in fp32 otherwise:
-    with A = sum p |v| and delta the error of a logit, d + 8 roundings of 2^-24 of
+    with A = sum p max(|v|, w), w [T, Hkv, 1] = `rounded` the size of what multiplies
+    the rounded probability where that is not v itself (a zero point is added apart:
+    v = code * scale + z), and delta the error of a logit, d + 8 roundings of 2^-24 of
     sigma sum |q_c k_c|, plus 2^-22 of the logit for its scaling and the exponential,
       2^-11 (A + |o|) + (2 delta + 2^-20 + T 2^-23) (A + |o|) + 2^-24.
     A row that sees nothing gives 0."""
@@ -71,7 +73,9 @@ def attention(q, k, v, see, scale: float | None = None):
             p = np.exp(x[i, j] - x[i, j].max())
             p /= p.sum()
             o[i, h] = p @ vh[j]
-            a = p @ np.abs(vh[j]) + np.abs(o[i, h])
+            size = np.abs(vh[j]) if rounded is None else np.maximum(np.abs(vh[j]),
+                                                                    rounded[j, h // G])
+            a = p @ size + np.abs(o[i, h])
             delta = (d + 8) * 2.0 ** -24 * big[i, j].max() + 2.0 ** -22 * np.abs(x[i, j]).max()
             bound[i, h] += (2.0 ** -11 + 2 * delta + 2.0 ** -20 + len(j) * 2.0 ** -23) * a
     return o, bound

@@ -27,7 +27,7 @@ class Case:
 
     def __init__(self, lens, hq, hkv, d, kbits, vb, asym=False, seed=0, gain=8.0, slots=None,
                  max_seqs=None, v_scale=1.0):
-        self.lens, self.hq, self.hkv, self.d, self.vb = lens, hq, hkv, d, vb
+        self.lens, self.hq, self.hkv, self.d, self.vb, self.asym = lens, hq, hkv, d, vb, asym
         self.rng = np.random.default_rng(seed)
         pages = sum(-(-t // 16) + len(kbits) for t in lens) * hkv + 1
         self.cache = ekv.Cache(1, max_seqs or len(lens), hq, hkv, d, max(max(lens), 16),
@@ -69,11 +69,22 @@ class Case:
                 kh, vh = self.state[z].khat(), self.state[z].vhat()
             want, tol = serving.attention(q[z, :c], np.concatenate([kh, k[z, :c]]),
                                           np.concatenate([vh, v[z, :c]]),
-                                          serving.tree_sees(par[z], c, t))
+                                          serving.tree_sees(par[z], c, t), rounded=self.sizes(vh, c))
             err = np.abs(o[z, :c].astype(np.float64) - want)
             assert np.all(err <= tol), f"sequence {z}: {np.max(err / tol):.2f} of the bound"
             worst = max(worst, float(np.max(err / tol)) if err.size else 0.0)
         return worst
+
+    def sizes(self, vh, c):
+        """What the rounded probability multiplies, where that is not the value: with the
+        asymmetric quantizer a value is code * s + (zero point), |code| <= 2^(b-1), and the
+        row's values span at least 2^b - 2 steps (its smallest and largest take the end
+        codes, at most one step short), so |code| s <= span * 2^(b-1) / (2^b - 2)."""
+        if not self.asym or self.vb == 16:
+            return None
+        span = vh.max(-1, keepdims=True) - vh.min(-1, keepdims=True) if len(vh) else vh[..., :1]
+        w = span * 2.0 ** (self.vb - 1) / (2.0 ** self.vb - 2)
+        return np.concatenate([w, np.zeros((c, self.hkv, 1))])
 
     def run(self, m, shape="tree", cnt=None, q_scale=1.0):
         q, k, v, par = self.drafts(m, shape, q_scale)
