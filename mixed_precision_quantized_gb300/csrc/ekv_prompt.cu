@@ -139,7 +139,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
                  kv_empty = kv_full + 8 * SLOTS;
   volatile int* stop = reinterpret_cast<volatile int*>(bars + 12 + 2 * SLOTS);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 12 + 2 * SLOTS) + 1;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   for (int z = tid; z < A.n_seqs; z += PT) {
     const int a = A.cu[z], b = A.cu[z + 1];
@@ -167,7 +167,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = *s_tmem;  // columns: S0/P0 0.., S1/P1 128.., O0 256.., O1 256 + D..
+  const uint32_t tm = uniform(*s_tmem);  // columns: S0/P0 0.., S1/P1 128.., O0 256.., O1 256 + D..
   for (int z = tid; z < A.n_seqs; z += PT) {  // rank by length, longest first
     const int mine = levels_of(A, tb.len[z]);
     int rank = 0;
@@ -194,7 +194,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
           int mt, h;
           if (!cur.tile(A, tb, t, mt, h)) continue;
           nk = max(nk, mt + 1);
-          if (!bar_wait(q_empty + 8 * t, (qph >> t) & 1, stop)) break;
+          if (!warp_wait(q_empty + 8 * t, (qph >> t) & 1, stop)) break;
           qph ^= 1u << t;
           if (lane == 0) {
             bar_expect(q_full + 8 * t, TILE);
@@ -206,7 +206,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         for (int i = 0; i < 2 * nk && !*stop; ++i) {  // K0, V0, K1, V1, ...
           const int j = i >> 1;
           const bool is_v = i & 1;
-          if (!bar_wait(kv_empty + 8 * slot, ph, stop)) break;
+          if (!warp_wait(kv_empty + 8 * slot, ph, stop)) break;
           const uint32_t dst = sb + Cfg::KV_OFF + slot * TILE;
           const int left = len - j * BM;  // rows of the sequence from this tile's first
           const bool cut = is_v && left < BM;
@@ -217,7 +217,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
               tma_3d(dst + s * SUB, is_v ? &mv : &mk, s * 64, cur.head, start + j * BM, bar);
           }
           if (cut) {  // zero the rows behind the sequence, then hand the tile over
-            if (!bar_wait(tail, tph, stop)) break;
+            if (!warp_wait(tail, tph, stop)) break;
             tph ^= 1;
             uint8_t* v = smem + Cfg::KV_OFF + slot * TILE;
             for (int s = 0; s < NSUB; ++s)
@@ -239,10 +239,12 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
       constexpr uint32_t ID_S = idesc_f16(BM, BM, false), ID_O = idesc_f16(BM, D, true);
       int slot = 0;
       uint32_t ph = 0, qph = 0, pph = 0;
+      bool ok = true;
       auto scores = [&](int t, int ks) {
-        const uint32_t a = sb + Cfg::Q_OFF + t * TILE, b = sb + Cfg::KV_OFF + ks * TILE;
-        if (lane == 0) {
-  #pragma unroll
+        const uint32_t a = sb + Cfg::Q_OFF + t * TILE;
+        const uint32_t b = uniform(sb + Cfg::KV_OFF + ks * TILE);
+        if (elect()) {
+#pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = (k / 4) * SUB + (k % 4) * 32;
             mma_ss(tm + t * BM, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), ID_S,
@@ -252,7 +254,32 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         }
         __syncwarp();
       };
-      while (cur.next(A, tb) && !*stop) {
+      auto values = [&](int t, int vs, bool first) {
+        const uint32_t b = uniform(sb + Cfg::KV_OFF + vs * TILE);
+        const bool acc = uniform(!first);
+        if (elect()) {
+#pragma unroll
+          for (int k = 0; k < BM / 16; ++k)
+            mma_ts(tm + 256 + t * D, tm + t * BM + k * 8, desc_sw128(b + k * 2048, SUB, 1024), ID_O,
+                   acc || k > 0);
+          mma_commit(o_done + 8 * t);
+        }
+        __syncwarp();
+      };
+      auto release = [&](uint32_t bar) {
+        if (elect()) mma_commit(bar);
+        __syncwarp();
+      };
+      auto wait_tile = [&]() {  // the ring's next tile; returns its slot
+        ok = ok && warp_wait(kv_full + 8 * slot, ph, stop);
+        const int at = slot;
+        if (++slot == SLOTS) {
+          slot = 0;
+          ph ^= 1;
+        }
+        return at;
+      };
+      while (ok && cur.next(A, tb)) {
         int nk[2] = {0, 0};
         for (int t = 0; t < 2; ++t) {
           int mt, h;
@@ -260,65 +287,37 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         }
         const int n = max(nk[0], nk[1]);
         if (n == 0) continue;
-        bool ok = bar_wait(kv_full + 8 * slot, ph, stop);
-        int ks = slot;
+        int ks = wait_tile();
         for (int t = 0; t < 2 && ok; ++t) {
           if (!nk[t]) continue;
-          ok = bar_wait(q_full + 8 * t, (qph >> t) & 1, stop);
+          ok = warp_wait(q_full + 8 * t, (qph >> t) & 1, stop);
           qph ^= 1u << t;
           fence_after();
-          if (ok) scores(t, ks);
-          if (lane == 0 && ok && nk[t] == 1) mma_commit(q_empty + 8 * t);
+          if (!ok) break;
+          scores(t, ks);
+          if (nk[t] == 1) release(q_empty + 8 * t);
         }
         if (!ok) break;
-        if (lane == 0) mma_commit(kv_empty + 8 * ks);
-        if (++slot == SLOTS) {
-          slot = 0;
-          ph ^= 1;
-        }
+        release(kv_empty + 8 * ks);
         for (int j = 0; j < n && ok; ++j) {
-          ok = bar_wait(kv_full + 8 * slot, ph, stop);
-          const int vs = slot;
-          if (++slot == SLOTS) {
-            slot = 0;
-            ph ^= 1;
-          }
-          if (!ok) break;
-          if (j + 1 < n) {
-            ks = slot;
-            ok = bar_wait(kv_full + 8 * slot, ph, stop);
-            if (++slot == SLOTS) {
-              slot = 0;
-              ph ^= 1;
-            }
-            if (!ok) break;
-          }
-          for (int t = 0; t < 2; ++t) {
+          const int vs = wait_tile();
+          if (j + 1 < n) ks = wait_tile();
+          for (int t = 0; t < 2 && ok; ++t) {
             if (j >= nk[t]) continue;
-            ok = bar_wait(p_full + 8 * t, (pph >> t) & 1, stop);
+            ok = warp_wait(p_full + 8 * t, (pph >> t) & 1, stop);
             if (!ok) break;
             pph ^= 1u << t;
             fence_after();
-            if (lane == 0) {
-              const uint32_t b = sb + Cfg::KV_OFF + vs * TILE;
-  #pragma unroll
-              for (int k = 0; k < BM / 16; ++k)
-                mma_ts(tm + 256 + t * D, tm + t * BM + k * 8, desc_sw128(b + k * 2048, SUB, 1024), ID_O,
-                       j > 0 || k > 0);
-              mma_commit(o_done + 8 * t);
-            }
-            __syncwarp();
+            values(t, vs, j == 0);
             if (j + 1 < nk[t]) {
               scores(t, ks);
-              if (lane == 0 && j + 2 == nk[t]) mma_commit(q_empty + 8 * t);
+              if (j + 2 == nk[t]) release(q_empty + 8 * t);
             }
           }
-          if (lane == 0 && ok) {
-            mma_commit(kv_empty + 8 * vs);
-            if (j + 1 < n) mma_commit(kv_empty + 8 * ks);
-          }
+          if (!ok) break;
+          release(kv_empty + 8 * vs);
+          if (j + 1 < n) release(kv_empty + 8 * ks);
         }
-        if (!ok) break;
       }
     }
   } else {
@@ -340,8 +339,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
       uint64_t l2 = pack2(0.f, 0.f);
       bool ok = !*stop;
       for (int j = 0; j < nk && ok; ++j) {
-        ok = bar_wait(s_full + 8 * t, sph, stop);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(s_full + 8 * t, sph, stop);
         if (!ok) break;
         sph ^= 1;
         fence_after();
@@ -368,7 +366,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
           // O holds the products up to tile j - 1: wait for them, rescale this row
           const float f = move ? ex2(mref - mnew) : 1.f;
           if (move) mref = mnew;
-          ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+          ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
           if (!ok) break;
           fence_after();
           l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
@@ -403,7 +401,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         oph ^= 1;  // the phase that this tile's product completes, inverted
       }
       // O / l; NaN if a wait gave up
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+      if (ok) ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
       fence_after();
       const int i = mt * BM + row;
       float la, lb;

@@ -15,6 +15,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// One thread of a converged warp.  tcgen05.mma and its descriptors live in uniform
+// registers: behind this predicate, with operands that are the same in every lane (see
+// `uniform`), an MMA issues in ~20 cycles; behind a per-lane branch each one takes ~50
+// (measured: 64-column products 35 and 49 cycles apart).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{ .reg .pred P; elect.sync _|P, 0xffffffff; selp.b32 %0, 1, 0, P; }" : "=r"(p));
+  return p != 0;
+}
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // ---- mbarrier --------------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -47,6 +61,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   }
   *stop = 1;
   return false;
+}
+
+// The same for a whole warp, with one outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, stop));
 }
 
 // ---- TMA -------------------------------------------------------------------------

@@ -11,11 +11,11 @@
 // (1 to 512), so each page is worth 16 keys to all of them: it is read from memory and
 // unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
 // tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
-//   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
-//   warps 8-15   unpack a raw tile into swizzled fp16 operand tiles: K as hi + lo
+//   warp 13      page copies (cp.async.bulk) into a ring of raw tiles
+//   warps 8-11   unpack a raw tile into swizzled fp16 operand tiles: K as hi + lo
 //                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K
 //                need hi alone), V as the bare codes (exact in fp16)
-//   warp 16      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
+//   warp 12      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
 //   warps 0-3, 4-7  two softmax streams, one row a thread
 // With more than 128 rows the two streams are two row tiles over the same tokens; with
 // fewer they are the even and odd token tiles of the same rows, merged at the end
@@ -44,22 +44,25 @@ using namespace tc;
 constexpr int TM_ROWS = 128;      // rows of a row tile
 constexpr int TN = 64;            // tokens of a token tile
 constexpr int TPAGES = TN / BLOCK;
-constexpr int TT = 640;           // threads
-// 96 registers a thread at launch (65,536 / 640, in eights: 61,440 in all); softmax takes
-// 128, unpacking 80, the rest 56: 256 x 128 + 256 x 80 + 128 x 56 = 60,416.
-constexpr int TREGS_SOFTMAX = 128, TREGS_UNPACK = 80, TREGS_OTHER = 56;
+constexpr int TT = 512;           // threads
+// 128 registers a thread at launch, all 65,536 of an SM; softmax takes 160, unpacking
+// keeps 128, the rest 64: 256 x 160 + 128 x 128 + 128 x 64.  (With 8 unpacking warps
+// the shares are too small: both they and the softmax warps spill.)
+constexpr int TREGS_SOFTMAX = 160, TREGS_OTHER = 64;
 constexpr int TSEQS = 512;        // sequences of one launch
-constexpr int TSTAGES = 2;        // operand tiles in flight
+constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
+constexpr int VST = 3;            // V operand tiles in flight (until their products are done)
 constexpr int RAW_BYTES = 96 * 1024;
 constexpr int RAW_MAX = 8;        // raw tiles in flight at most
-constexpr int DW = 8;             // unpacking warps
+constexpr int DW = TPAGES;        // unpacking warps, one a page
 
 template <int D>
 struct TCfg {
   static constexpr int SUBT = TN * 128;              // 64 channels of a tile
   static constexpr int OPND = D / 64 * SUBT;         // one operand tile
-  static constexpr int STAGE = 3 * OPND;             // K hi, K lo, V
-  static constexpr int RAW_OFF = TSTAGES * STAGE;
+  static constexpr int KSTAGE = 2 * OPND;            // hi, lo
+  static constexpr int V_OFF = KST * KSTAGE;
+  static constexpr int RAW_OFF = V_OFF + VST * OPND;
   static constexpr int MISC_OFF = RAW_OFF + RAW_BYTES;
 };
 
@@ -70,14 +73,14 @@ struct TMisc {
   uint8_t cnt[TSEQS];           // nodes
   unsigned long long anc[2][64];  // ancestors-or-self of each node, by segment parity
   // of each token's V scale s: log2 s, 1 / s and (asymmetric) the zero point over s
-  alignas(16) float lsv[TSTAGES][TN];
-  alignas(16) float rsv[TSTAGES][TN];
-  alignas(16) float zsv[TSTAGES][TN];
-  alignas(8) uint16_t valid[TSTAGES][TPAGES];  // tokens that are there
-  int32_t has_lo[TSTAGES];
-  int32_t ent[RAW_MAX][TPAGES];
+  alignas(16) float lsv[VST][TN];
+  alignas(16) float rsv[VST][TN];
+  alignas(16) float zsv[VST][TN];
+  alignas(8) uint16_t valid[VST][TPAGES];  // tokens that are there
+  int32_t has_lo[KST];
+  alignas(16) int32_t ent[RAW_MAX][TPAGES];
   float ml[2][3][TM_ROWS];      // (m, l, z) of the two streams
-  alignas(8) uint64_t bars[2 * TSTAGES + 2 * RAW_MAX + 4 * 2];
+  alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 4 * 2];
   int stop;
   uint32_t tmem;
 };
@@ -207,22 +210,39 @@ constexpr uint32_t MAGIC = 0x64006400u;   // fp16 1024, 1024
 // power of two that a code's position in the word multiplies it by.
 __device__ __forceinline__ constexpr uint32_t both(uint32_t h) { return h | h << 16; }
 
-// Codes of B bits (signed q for the symmetric quantizer, unsigned u for the other), or raw
-// fp16 for B = 16.  `row` points at the row's first byte.
+// A row's 8 codes of group g as stored (raw fp16 for B = 16), and what they unpack to:
+// signed codes q for the symmetric quantizer, unsigned u for the other.
+template <int B>
+struct Raw8 {
+  uint32_t x[B == 16 ? 4 : B == 8 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* row, int g) {
+    if constexpr (B == 16) {
+      const uint4 u = *reinterpret_cast<const uint4*>(row + 16 * g);
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    } else if constexpr (B == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(row + 8 * g);
+      x[0] = u.x; x[1] = u.y;
+    } else if constexpr (B == 4) {
+      x[0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
+    } else {
+      x[0] = *reinterpret_cast<const uint16_t*>(row + 2 * g);
+    }
+  }
+};
 template <int B, bool ASYM>
-__device__ __forceinline__ void unpack8w(const uint8_t* row, int g, uint32_t* w) {
+__device__ __forceinline__ void unpack8w(const Raw8<B>& c, uint32_t* w) {
   if constexpr (B == 16) {
-    perm8(*reinterpret_cast<const uint4*>(row + 16 * g), w);
+    perm8(make_uint4(c.x[0], c.x[1], c.x[2], c.x[3]), w);
   } else if constexpr (B == 8) {
-    const uint2 r = *reinterpret_cast<const uint2*>(row + 8 * g);
-    const uint32_t y0 = __byte_perm(r.x, r.y, 0x5140), y1 = __byte_perm(r.x, r.y, 0x7362);
+    const uint32_t y0 = __byte_perm(c.x[0], c.x[1], 0x5140);
+    const uint32_t y1 = __byte_perm(c.x[0], c.x[1], 0x7362);
     const uint32_t sub = both(ASYM ? 0x6400 : 0x6480);  // 1024 or 1152
     w[0] = hsub(__byte_perm(y0, 0x64646464u, 0x4140), sub);
     w[1] = hsub(__byte_perm(y0, 0x64646464u, 0x4342), sub);
     w[2] = hsub(__byte_perm(y1, 0x64646464u, 0x4140), sub);
     w[3] = hsub(__byte_perm(y1, 0x64646464u, 0x4342), sub);
   } else if constexpr (B == 4) {
-    const uint32_t r = *reinterpret_cast<const uint32_t*>(row + 4 * g), r8 = r >> 8;
+    const uint32_t r = c.x[0], r8 = r >> 8;
     const uint32_t lo = both(ASYM ? 0x6400 : 0x6408);   // 1024 or 1032
     const uint32_t hi = both(ASYM ? 0xD400 : 0xD480);   // -64 or -72
     const uint32_t q16 = both(0x2C00);                  // 1/16
@@ -231,8 +251,7 @@ __device__ __forceinline__ void unpack8w(const uint8_t* row, int g, uint32_t* w)
     w[2] = hsub(and_or(r8, 0x000F000Fu, MAGIC), lo);
     w[3] = hfma(and_or(r8, 0x00F000F0u, MAGIC), q16, hi);
   } else {
-    const uint32_t r = *reinterpret_cast<const uint16_t*>(row + 2 * g);
-    const uint32_t x = __byte_perm(r, 0, 0x4140);
+    const uint32_t x = __byte_perm(c.x[0], 0, 0x4140);
     w[0] = hsub(and_or(x, 0x00030003u, MAGIC), both(ASYM ? 0x6400 : 0x6402));
     w[1] = hfma(and_or(x, 0x000C000Cu, MAGIC), both(0x3400), both(ASYM ? 0xDC00 : 0xDC08));
     w[2] = hfma(and_or(x, 0x00300030u, MAGIC), both(0x2C00), both(ASYM ? 0xD400 : 0xD420));
@@ -263,71 +282,84 @@ __device__ __forceinline__ uint32_t tile_at(int row, int g) {  // 16-byte chunk 
   return (g >> 3) * TCfg<D>::SUBT + row * 128 + (((g & 7) ^ (row & 7)) << 4);
 }
 
-// One warp unpacks half of a page's 16 rows (tile rows r0 ..): group g of rows t0, t0 +
-// step, ...; rows from `n` on hold no token (K left as it is, V zero).
+// A warp unpacks a page: group g of rows t0, t0 + STEP, ... (lanes side by side over the
+// groups of a row).  FULL: every row holds a token; else rows from n on
+// do not (K left as it is, V zero).
 template <int D>
-struct Half {
-  static constexpr int GR = D / 8, LANES = 32 / GR;  // groups, rows side by side
-  int g, t0, step, nrow;
-  __device__ Half(int half, int lane) {
-    g = lane % GR;
-    t0 = half * LANES + lane / GR;
-    step = 2 * LANES;
-    nrow = BLOCK / (2 * LANES);
-  }
+struct Lane {
+  static constexpr int GR = D / 8, STEP = 32 / GR;
+  int g, t0;
+  __device__ Lane(int lane) : g(lane % GR), t0(lane / GR) {}
 };
 
-template <int D, int KB, bool ASYM>
+template <int D, int KB, bool ASYM, bool FULL>
 __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int n, uint8_t* hi,
-                                         uint8_t* lo, bool want_lo, int r0, const Half<D>& hf) {
+                                         bool want_lo, int r0, const Lane<D>& hf) {
+  constexpr int STEP = Lane<D>::STEP;
   uint32_t sc[4], zp[4];
   if constexpr (KB < 16) {
     channel8<KB>(kp + BLOCK * D * KB / 8, hf.g, sc);
     if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, hf.g, zp);
   }
+#pragma unroll 1
+  for (int t4 = hf.t0; t4 < BLOCK; t4 += 4 * STEP) {  // 4 rows at once
+    Raw8<KB> raw[4];
 #pragma unroll
-  for (int i = 0; i < 16 / (2 * Half<D>::LANES); ++i) {
-    const int t = hf.t0 + i * hf.step;
-    if (t >= n) break;
-    uint32_t w[4], l[4] = {0, 0, 0, 0};
-    unpack8w<KB, ASYM>(kp + t * stride, hf.g, w);
-    if constexpr (KB < 16 && !ASYM) {
+    for (int i = 0; i < 4; ++i)
+      if (FULL || t4 + i * STEP < n) raw[i].load(kp + (t4 + i * STEP) * stride, hf.g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t p = hmul(w[j], sc[j]);
-        if constexpr (KB > 2) l[j] = hfma(w[j], sc[j], hneg(p));  // exact residual
-        w[j] = p;
+    for (int i = 0; i < 4; ++i) {
+      const int t = t4 + i * STEP;
+      if (!FULL && t >= n) break;
+      uint32_t w[4], l[4] = {0, 0, 0, 0};
+      unpack8w<KB, ASYM>(raw[i], w);
+      if constexpr (KB < 16 && !ASYM) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t p = hmul(w[j], sc[j]);
+          if constexpr (KB > 2) l[j] = hfma(w[j], sc[j], hneg(p));  // exact residual
+          w[j] = p;
+        }
+      } else if constexpr (KB < 16) {  // u s + z in fp32, then hi + lo
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = __half22float2(*reinterpret_cast<__half2*>(&w[j]));
+          const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[j]));
+          const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[j]));
+          const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
+          const __half2 p = __floats2half2_rn(a, b);
+          const float2 pf = __half22float2(p);
+          const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
+          w[j] = *reinterpret_cast<const uint32_t*>(&p);
+          l[j] = *reinterpret_cast<const uint32_t*>(&r);
+        }
       }
-    } else if constexpr (KB < 16) {  // u s + z in fp32, then hi + lo
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 u = __half22float2(*reinterpret_cast<__half2*>(&w[j]));
-        const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[j]));
-        const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[j]));
-        const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
-        const __half2 p = __floats2half2_rn(a, b);
-        const float2 pf = __half22float2(p);
-        const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
-        w[j] = *reinterpret_cast<const uint32_t*>(&p);
-        l[j] = *reinterpret_cast<const uint32_t*>(&r);
-      }
+      uint8_t* at = hi + tile_at<D>(r0 + t, hf.g);
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (want_lo)
+        *reinterpret_cast<uint4*>(at + TCfg<D>::OPND) = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    const uint32_t at = tile_at<D>(r0 + t, hf.g);
-    *reinterpret_cast<uint4*>(hi + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (want_lo) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 // V codes are signed for both quantizers: u s + z = (u - 2^(b-1)) s + (z + 2^(b-1) s), so
 // that the products P' q stay as small as the values.
-template <int D, int VB>
+template <int D, int VB, bool FULL>
 __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int n, uint8_t* dst,
-                                         int r0, const Half<D>& hf) {
+                                         int r0, const Lane<D>& hf) {
+  constexpr int STEP = Lane<D>::STEP;
+#pragma unroll 1
+  for (int t4 = hf.t0; t4 < BLOCK; t4 += 4 * STEP) {
+    Raw8<VB> raw[4];
 #pragma unroll
-  for (int i = 0; i < 16 / (2 * Half<D>::LANES); ++i) {
-    const int t = hf.t0 + i * hf.step;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (t < n) unpack8w<VB, false>(vp + t * stride, hf.g, w);
-    *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i)
+      if (FULL || t4 + i * STEP < n) raw[i].load(vp + (t4 + i * STEP) * stride, hf.g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t4 + i * STEP;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (FULL || t < n) unpack8w<VB, false>(raw[i], w);
+      *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -338,10 +370,12 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   TMisc& M = *reinterpret_cast<TMisc*>(smem + Cfg::MISC_OFF);
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t b0 = smem_u32(M.bars);
-  const uint32_t tile_full = b0, tile_empty = b0 + 8 * TSTAGES, raw_full = tile_empty + 8 * TSTAGES,
-                 raw_empty = raw_full + 8 * RAW_MAX, q_full = raw_empty + 8 * RAW_MAX,
+  const uint32_t k_full = b0, k_empty = k_full + 8 * KST, v_full = k_empty + 8 * KST,
+                 v_empty = v_full + 8 * VST, sc_full = v_empty + 8 * VST,
+                 raw_full = sc_full + 8 * VST, raw_empty = raw_full + 8 * RAW_MAX,
+                 q_full = raw_empty + 8 * RAW_MAX,
                  s_full = q_full + 16, p_full = s_full + 16, o_done = p_full + 16;
   volatile int* stop = &M.stop;
 
@@ -355,9 +389,14 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     M.cnt[z] = (uint8_t)cnt;
   }
   if (tid == 0) {
-    for (int i = 0; i < TSTAGES; ++i) {
-      bar_init(tile_full + 8 * i, DW);
-      bar_init(tile_empty + 8 * i, 1);
+    for (int i = 0; i < KST; ++i) {
+      bar_init(k_full + 8 * i, DW);
+      bar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < VST; ++i) {
+      bar_init(v_full + 8 * i, DW);
+      bar_init(v_empty + 8 * i, 1);
+      bar_init(sc_full + 8 * i, TPAGES);
     }
     for (int i = 0; i < RAW_MAX; ++i) {
       bar_init(raw_full + 8 * i, 1);
@@ -372,11 +411,12 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     M.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tmem_alloc(smem_u32(&M.tmem), 512);
+  if (warp == 12) tmem_alloc(smem_u32(&M.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = M.tmem;  // stream t at 256 t: Q (D / 2 columns), S and P at 64, O at 128
+  // Stream t at column 256 t: Q (D / 2 columns), S and P at 64, O at 128.
+  const uint32_t tm = uniform(M.tmem);
   if (warp == 0) {             // prefix of the sequences' costs
     int64_t run = 0;
     for (int z0 = 0; z0 < A.n_seqs; z0 += 32) {
@@ -398,7 +438,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   }
   __syncthreads();
 
-  if (warp >= 16) {
+  if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_OTHER));
     Walk w;
     w.init(M, A.n_seqs, A.grid);
@@ -406,7 +446,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     const int kmax = max(2, st.kmax[A.layer]);
     const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
     const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-    if (warp == 17) {
+    if (warp == 13) {
       // ---- page copies ---------------------------------------------------------------
       int rs = 0;
       uint32_t ph = 1;
@@ -422,7 +462,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             const int b = i * TPAGES + lane;
             ahead = b < nblk ? bt[b] : -1;
           }
-          ok = bar_wait(raw_empty + 8 * rs, ph, stop);
+          ok = warp_wait(raw_empty + 8 * rs, ph, stop);
           if (!ok) break;
           const int32_t e = __shfl_sync(0xffffffffu, ahead, k * TPAGES + (lane & 3));
           const int b = i * TPAGES + (lane & 3);
@@ -453,20 +493,22 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
         }
       }
-    } else if (warp == 16) {
+    } else if (warp == 12) {
       // ---- products ------------------------------------------------------------------
       constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false), ID_O = idesc_f16(TM_ROWS, D, true);
-      int stage = 0;
-      uint32_t fph = 0, qph = 0, pph = 0;
+      int ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0, qph = 0, pph = 0;
       bool ok = true;
       auto scores = [&](int t, int sg) {
-        const uint32_t base = sb + sg * Cfg::STAGE, d = tm + 256 * t + 64, q = tm + 256 * t;
-        if (lane == 0) {
+        const uint32_t base = uniform(sb + sg * Cfg::KSTAGE);
+        const uint32_t d = uniform(tm + 256 * t + 64), q = uniform(tm + 256 * t);
+        const bool lo = uniform(M.has_lo[sg]) != 0;
+        if (elect()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ts(d, q + 8 * k,
                    desc_sw128(base + (k / 4) * Cfg::SUBT + (k % 4) * 32, 16, 1024), ID_S, k > 0);
-          if (M.has_lo[sg]) {
+          if (lo) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_ts(d, q + 8 * k,
@@ -478,123 +520,140 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         __syncwarp();
       };
       auto values = [&](int t, int sg, bool first) {
-        const uint32_t base = sb + sg * Cfg::STAGE + 2 * Cfg::OPND;
-        if (lane == 0) {
+        const uint32_t base = uniform(sb + Cfg::V_OFF + sg * Cfg::OPND);
+        const uint32_t d = uniform(tm + 256 * t + 128), p = uniform(tm + 256 * t + 64);
+        const bool acc = uniform(!first);
+        if (elect()) {
 #pragma unroll
           for (int k = 0; k < TN / 16; ++k)
-            mma_ts(tm + 256 * t + 128, tm + 256 * t + 64 + 8 * k,
-                   desc_sw128(base + k * 2048, Cfg::SUBT, 1024), ID_O, !first || k > 0);
+            mma_ts(d, p + 8 * k, desc_sw128(base + k * 2048, Cfg::SUBT, 1024), ID_O, acc || k > 0);
           mma_commit(o_done + 8 * t);
         }
         __syncwarp();
       };
-      auto wait_tile = [&]() {  // the next operand tile; returns its stage
-        ok = ok && bar_wait(tile_full + 8 * stage, fph, stop);
-        const int sg = stage;
-        if (++stage == TSTAGES) {
-          stage = 0;
-          fph ^= 1;
+      auto release = [&](uint32_t bar) {
+        if (elect()) mma_commit(bar);
+        __syncwarp();
+      };
+      auto next_k = [&]() {  // wait for the next K tile; returns its stage
+        ok = ok && warp_wait(k_full + 8 * ks, kph, stop);
+        fence_after();
+        const int sg = ks;
+        if (++ks == KST) {
+          ks = 0;
+          kph ^= 1;
+        }
+        return sg;
+      };
+      auto next_v = [&]() {
+        ok = ok && warp_wait(v_full + 8 * vs, vph, stop);
+        fence_after();
+        const int sg = vs;
+        if (++vs == VST) {
+          vs = 0;
+          vph ^= 1;
         }
         return sg;
       };
       auto wait_on = [&](uint32_t bar, uint32_t& bits, int t) {
-        ok = ok && bar_wait(bar + 8 * t, (bits >> t) & 1, stop);
+        ok = ok && warp_wait(bar + 8 * t, (bits >> t) & 1, stop);
         bits ^= 1u << t;
         fence_after();
       };
       while (ok && w.next(M, st.G, st.Hkv)) {
         const int n = w.e - w.s;
-        if (w.nrt == 2) {
-          int sg = wait_tile();
-          for (int t = 0; t < 2; ++t) {
-            wait_on(q_full, qph, t);
-            if (ok) scores(t, sg);
-          }
+        wait_on(q_full, qph, 0);
+        wait_on(q_full, qph, 1);
+        if (w.nrt == 2) {  // both streams take every tile
+          int kg = next_k();
+          if (!ok) break;
+          scores(0, kg);
+          scores(1, kg);
+          release(k_empty + 8 * kg);
           for (int i = 0; i < n && ok; ++i) {
-            const int nx = i + 1 < n ? wait_tile() : 0;
+            const int vg = next_v();
+            if (i + 1 < n) kg = next_k();
             for (int t = 0; t < 2 && ok; ++t) {
               wait_on(p_full, pph, t);
               if (!ok) break;
-              values(t, sg, i == 0);
-              if (i + 1 < n) scores(t, nx);
+              values(t, vg, i == 0);
+              if (i + 1 < n) scores(t, kg);
             }
-            if (ok && lane == 0) mma_commit(tile_empty + 8 * sg);
-            sg = nx;
+            if (!ok) break;
+            release(v_empty + 8 * vg);
+            if (i + 1 < n) release(k_empty + 8 * kg);
           }
-        } else {
-          wait_on(q_full, qph, 0);
-          wait_on(q_full, qph, 1);
-          int sg = wait_tile();
-          if (ok) scores(0, sg);
+        } else {  // the streams take turns
+          int kg = next_k();
+          if (!ok) break;
+          scores(0, kg);
+          release(k_empty + 8 * kg);
           for (int i = 0; i < n && ok; ++i) {
             const int t = i & 1;
-            int nx = 0;
             if (i + 1 < n) {
-              nx = wait_tile();
-              fence_after();
-              if (ok) scores(t ^ 1, nx);
+              kg = next_k();
+              if (!ok) break;
+              scores(t ^ 1, kg);
+              release(k_empty + 8 * kg);
             }
+            const int vg = next_v();
             wait_on(p_full, pph, t);
             if (!ok) break;
-            values(t, sg, i < 2);
-            if (lane == 0) mma_commit(tile_empty + 8 * sg);
-            sg = nx;
+            values(t, vg, i < 2);
+            release(v_empty + 8 * vg);
           }
         }
       }
     }
   } else if (warp >= 8) {
     // ---- unpacking -------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_UNPACK));
     Walk w;
     w.init(M, A.n_seqs, A.grid);
     const int kmax = max(2, st.kmax[A.layer]);
     const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
     const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-    const int pg = (warp - 8) >> 1;  // page of the tile
-    const Half<D> hf(warp & 1, lane);
-    int rs = 0, stage = 0;
-    uint32_t rph = 0, eph = 1;
+    const int pg = warp - 8;  // page of the tile
+    const Lane<D> hf(lane);
+    const int r0 = pg * BLOCK;
+    int rs = 0, ks = 0, vs = 0;
+    uint32_t rph = 0, keph = 1, veph = 1;
     bool ok = true;
     while (ok && w.next(M, st.G, st.Hkv)) {
       const __half* stg = st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
       for (int i = w.s; i < w.e && ok; ++i) {
         const bool drafts = i == w.nt - 1;
-        if (!drafts) ok = bar_wait(raw_full + 8 * rs, rph, stop);
-        ok = ok && bar_wait(tile_empty + 8 * stage, eph, stop);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t* hi = smem + stage * Cfg::STAGE;
-        uint8_t* lo = hi + Cfg::OPND;
-        uint8_t* vt = lo + Cfg::OPND;
-        const int blk = i * TPAGES + pg;
-        // where the page's rows are, how many hold tokens, and whether the tile needs lo
+        if (!drafts) ok = warp_wait(raw_full + 8 * rs, rph, stop);
+        // Where the page's rows are, how many hold tokens, and whether the tile needs lo.
         int kb = 16, vb = A.vb, n = 0;
-        bool want_lo = false;
+        bool want_lo = false, full = false;
         const uint8_t *kp = nullptr, *vp = nullptr;
-        int64_t ks, vs;
+        int64_t kst = 2 * D, vst = D * vb / 8;
+        const int raw = Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
+        int rawv = raw;
         if (drafts) {
           n = min(BLOCK, max(0, w.cnt - BLOCK * pg));
           const size_t at = (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
           kp = reinterpret_cast<const uint8_t*>(A.k + at);
           vp = reinterpret_cast<const uint8_t*>(A.v + at);
           vb = 16;
-          ks = vs = (int64_t)st.Hkv * D * 2;
-        } else {
+          kst = vst = (int64_t)st.Hkv * D * 2;
+        } else if (ok) {
+          const int4 ent = *reinterpret_cast<const int4*>(M.ent[rs]);
+          const int32_t es[TPAGES] = {ent.x, ent.y, ent.z, ent.w};
+          int32_t e = -1;
+#pragma unroll
           for (int x = 0; x < TPAGES; ++x) {
-            const int32_t e = M.ent[rs][x];
-            const int b = bits_of_code(entry_fmt(e) >> 2);
-            if (e != -1 && (i * TPAGES + x + 1) * BLOCK <= w.len)
+            const int b = bits_of_code(entry_fmt(es[x]) >> 2);
+            if (es[x] != -1 && (i * TPAGES + x + 1) * BLOCK <= w.len)
               want_lo |= b < 16 && (ASYM || b > 2);
+            if (x == pg) e = es[x];
           }
-          const int32_t e = M.ent[rs][pg];
-          n = e == -1 ? 0 : min(BLOCK, w.len - blk * BLOCK);
+          n = e == -1 ? 0 : min(BLOCK, w.len - (i * TPAGES + pg) * BLOCK);
           if (n > 0) {
-            const int fmt = entry_fmt(e);
-            const int pkb = bits_of_code(fmt >> 2);
-            kp = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
-            vp = kp + k_part_bytes(pkb, D, ASYM);
-            if (n == BLOCK) {
+            const int fmt = entry_fmt(e), pkb = bits_of_code(fmt >> 2);
+            rawv = raw + k_part_bytes(pkb, D, ASYM);
+            full = n == BLOCK;
+            if (full) {
               kb = pkb;
             } else {  // the open block: raw K rows, V in the page, both read from memory
               kp = reinterpret_cast<const uint8_t*>(stg);
@@ -602,49 +661,76 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                    k_part_bytes(pkb, D, ASYM);
             }
           }
-          ks = D * kb / 8;
-          vs = D * vb / 8;
         }
-        const int r0 = pg * BLOCK;
-        switch (kb) {
-          case 2: unpack_k<D, 2, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
-          case 4: unpack_k<D, 4, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
-          case 8: unpack_k<D, 8, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
-          default: unpack_k<D, 16, ASYM>(kp, ks, n, hi, lo, want_lo, r0, hf); break;
-        }
-        switch (vb) {
-          case 2: unpack_v<D, 2>(vp, vs, n, vt, r0, hf); break;
-          case 4: unpack_v<D, 4>(vp, vs, n, vt, r0, hf); break;
-          case 8: unpack_v<D, 8>(vp, vs, n, vt, r0, hf); break;
-          default: unpack_v<D, 16>(vp, vs, n, vt, r0, hf); break;
-        }
-        if (!(warp & 1)) {
-          if (lane < BLOCK) {  // scale of token `lane` (rows of scale 0 hold zero codes only)
-            float s = 1.f, zv = 0.f;
-            if (vb < 16 && lane < n) {
-              const __half* sp = reinterpret_cast<const __half*>(vp + BLOCK * D * vb / 8);
-              s = __half2float(sp[lane]);
-              if (ASYM) zv = fmaf(s, (float)(1 << (vb - 1)), __half2float(sp[BLOCK + lane]));
-              if (s == 0.f) s = 1.f;
-            }
-            M.lsv[stage][r0 + lane] = log2f(s);
-            M.rsv[stage][r0 + lane] = 1.f / s;
-            if (ASYM) M.zsv[stage][r0 + lane] = zv / s;
+        // Scales first: softmax needs them with the scores.
+        ok = ok && warp_wait(v_empty + 8 * vs, veph, stop);
+        if (!ok) break;
+        if (lane < BLOCK) {  // token `lane` (rows of scale 0 hold zero codes only)
+          float s = 1.f, zv = 0.f;
+          if (vb < 16 && lane < n) {
+            const __half* sp = full
+                ? reinterpret_cast<const __half*>(smem + rawv + BLOCK * D * vb / 8)
+                : reinterpret_cast<const __half*>(vp + BLOCK * D * vb / 8);
+            s = __half2float(sp[lane]);
+            if (ASYM) zv = fmaf(s, (float)(1 << (vb - 1)), __half2float(sp[BLOCK + lane]));
+            if (s == 0.f) s = 1.f;
           }
-          if (lane == 0) {
-            M.valid[stage][pg] = (uint16_t)((1u << n) - 1);
-            if (pg == 0) M.has_lo[stage] = want_lo;
+          const float r = __fdividef(1.f, s);
+          M.lsv[vs][r0 + lane] = __log2f(s);
+          M.rsv[vs][r0 + lane] = r;
+          if (ASYM) M.zsv[vs][r0 + lane] = zv * r;
+        }
+        if (lane == 0) M.valid[vs][pg] = (uint16_t)((1u << n) - 1);
+        __syncwarp();
+        if (lane == 0) bar_arrive(sc_full + 8 * vs);
+        ok = warp_wait(k_empty + 8 * ks, keph, stop);
+        if (!ok) break;
+        uint8_t* hi = smem + ks * Cfg::KSTAGE;
+        if (full) {
+          const uint8_t* sp = smem + raw;
+          switch (kb) {
+            case 2: unpack_k<D, 2, ASYM, true>(sp, D / 4, n, hi, want_lo, r0, hf); break;
+            case 4: unpack_k<D, 4, ASYM, true>(sp, D / 2, n, hi, want_lo, r0, hf); break;
+            case 8: unpack_k<D, 8, ASYM, true>(sp, D, n, hi, want_lo, r0, hf); break;
+            default: unpack_k<D, 16, ASYM, true>(sp, 2 * D, n, hi, want_lo, r0, hf); break;
+          }
+        } else if (n > 0) {
+          unpack_k<D, 16, ASYM, false>(kp, kst, n, hi, want_lo, r0, hf);
+        }
+        if (pg == 0 && lane == 0) M.has_lo[ks] = want_lo;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(k_full + 8 * ks);
+        uint8_t* vt = smem + Cfg::V_OFF + vs * Cfg::OPND;
+        if (full) {
+          const uint8_t* sp = smem + rawv;
+          switch (vb) {
+            case 2: unpack_v<D, 2, true>(sp, D / 4, n, vt, r0, hf); break;
+            case 4: unpack_v<D, 4, true>(sp, D / 2, n, vt, r0, hf); break;
+            case 8: unpack_v<D, 8, true>(sp, D, n, vt, r0, hf); break;
+            default: unpack_v<D, 16, true>(sp, 2 * D, n, vt, r0, hf); break;
+          }
+        } else {
+          switch (vb) {
+            case 2: unpack_v<D, 2, false>(vp, vst, n, vt, r0, hf); break;
+            case 4: unpack_v<D, 4, false>(vp, vst, n, vt, r0, hf); break;
+            case 8: unpack_v<D, 8, false>(vp, vst, n, vt, r0, hf); break;
+            default: unpack_v<D, 16, false>(vp, vst, n, vt, r0, hf); break;
           }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(tile_full + 8 * stage);
+          bar_arrive(v_full + 8 * vs);
           if (!drafts) bar_arrive(raw_empty + 8 * rs);
         }
-        if (++stage == TSTAGES) {
-          stage = 0;
-          eph ^= 1;
+        if (++ks == KST) {
+          ks = 0;
+          keph ^= 1;
+        }
+        if (++vs == VST) {
+          vs = 0;
+          veph ^= 1;
         }
         if (!drafts && ++rs == nraw) {
           rs = 0;
@@ -708,12 +794,13 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       uint64_t l2 = pack2(0.f, 0.f), z2 = pack2(0.f, 0.f);
       int done = 0;
       for (int i = split ? w.s + t : w.s; i < w.e; i += split ? 2 : 1) {
-        // The operand stage of a tile: stages go round over all of the CTA's tiles.
-        ok = ok && __all_sync(0xffffffffu, bar_wait(s_full + 8 * t, sph, stop));
+        // V stages (and the scales with them) go round over all of the CTA's tiles.
+        const int at = tiles_before + (i - w.s), sg = at % VST;
+        ok = ok && warp_wait(sc_full + 8 * sg, (at / VST) & 1, stop);
+        ok = ok && warp_wait(s_full + 8 * t, sph, stop);
         if (!ok) break;
         sph ^= 1;
         fence_after();
-        const int sg = (tiles_before + (i - w.s)) % TSTAGES;
         if (!idle) {
           uint32_t s[64];
           tmem_ld32(ts, s);
@@ -756,7 +843,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             const float f = move ? ex2(mref - mx) : 1.f;
             if (move) mref = mx;
             if (done > 0) {  // O holds this stream's products up to the tile before
-              ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+              ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
               if (!ok) break;
               fence_after();
               l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
@@ -804,7 +891,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         oph ^= 1;
         ++done;
       }
-      if (ok && done) ok = __all_sync(0xffffffffu, bar_wait(o_done + 8 * t, oph ^ 1, stop));
+      if (ok && done) ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
       fence_after();
       float la, lb, za, zb;
       unpack2(l2, la, lb);
@@ -879,7 +966,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     if (!ok && lane == 0) set_error(st, EKV_ETIMEOUT);
   }
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 12) {
     fence_after();
     if (*stop) {
       if (lane == 0) set_error(st, EKV_ETIMEOUT);
@@ -954,7 +1041,9 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
 
 template <int D>
 constexpr int tree_smem() {
-  return TCfg<D>::MISC_OFF + (int)sizeof(TMisc) + 1024;
+  constexpr int bytes = TCfg<D>::MISC_OFF + (int)sizeof(TMisc) + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+  return bytes;
 }
 
 template <int D, bool ASYM>
