@@ -11,11 +11,13 @@
 // (1 to 512), so each page is worth 16 keys to all of them: it is read from memory and
 // unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
 // tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
-//   warp 13      page copies (cp.async.bulk) into a ring of raw tiles
-//   warps 8-11   unpack a raw tile into swizzled fp16 operand tiles: K as hi + lo
-//                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K
-//                need hi alone), V as the bare codes (exact in fp16)
-//   warp 12      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
+//   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
+//   warps 8-11, 12-15  unpack the K and the V parts of a raw tile, a page a warp, into
+//                swizzled fp16 operand tiles: K as hi + lo (khat = code * scale = hi + lo
+//                exactly, two products; 2- and 16-bit K need hi alone), V as the bare
+//                codes (exact in fp16)
+//   warp 18      the V scales of a tile, for softmax
+//   warp 16      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
 //   warps 0-3, 4-7  two softmax streams, one row a thread
 // With more than 128 rows the two streams are two row tiles over the same tokens; with
 // fewer they are the even and odd token tiles of the same rows, merged at the end
@@ -44,17 +46,15 @@ using namespace tc;
 constexpr int TM_ROWS = 128;      // rows of a row tile
 constexpr int TN = 64;            // tokens of a token tile
 constexpr int TPAGES = TN / BLOCK;
-constexpr int TT = 512;           // threads
-// 128 registers a thread at launch, all 65,536 of an SM; softmax takes 160, unpacking
-// keeps 128, the rest 64: 256 x 160 + 128 x 128 + 128 x 64.  (With 8 unpacking warps
-// the shares are too small: both they and the softmax warps spill.)
-constexpr int TREGS_SOFTMAX = 160, TREGS_OTHER = 64;
+constexpr int TT = 640;           // threads
+// 96 registers a thread at launch (65,536 / 640, in eights: 61,440 in all); softmax takes
+// 128, unpacking 80, the rest 64: 256 x 128 + 256 x 80 + 128 x 64.
+constexpr int TREGS_SOFTMAX = 128, TREGS_UNPACK = 80, TREGS_OTHER = 64;
 constexpr int TSEQS = 512;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
 constexpr int VST = 3;            // V operand tiles in flight (until their products are done)
 constexpr int RAW_BYTES = 96 * 1024;
 constexpr int RAW_MAX = 8;        // raw tiles in flight at most
-constexpr int DW = TPAGES;        // unpacking warps, one a page
 
 template <int D>
 struct TCfg {
@@ -78,7 +78,8 @@ struct TMisc {
   alignas(16) float zsv[VST][TN];
   alignas(8) uint16_t valid[VST][TPAGES];  // tokens that are there
   int32_t has_lo[KST];
-  alignas(16) int32_t ent[RAW_MAX][TPAGES];
+  alignas(16) int32_t ent[RAW_MAX][TPAGES];  // page-table entries of a raw tile
+  int32_t raw_lo[RAW_MAX];                   // whether its K needs the lo products
   float ml[2][3][TM_ROWS];      // (m, l, z) of the two streams
   alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 4 * 2];
   int stop;
@@ -301,14 +302,15 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
     channel8<KB>(kp + BLOCK * D * KB / 8, hf.g, sc);
     if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, hf.g, zp);
   }
+  constexpr int R = 2;  // rows at once
 #pragma unroll 1
-  for (int t4 = hf.t0; t4 < BLOCK; t4 += 4 * STEP) {  // 4 rows at once
-    Raw8<KB> raw[4];
+  for (int t4 = hf.t0; t4 < BLOCK; t4 += R * STEP) {
+    Raw8<KB> raw[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
       if (FULL || t4 + i * STEP < n) raw[i].load(kp + (t4 + i * STEP) * stride, hf.g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       const int t = t4 + i * STEP;
       if (!FULL && t >= n) break;
       uint32_t w[4], l[4] = {0, 0, 0, 0};
@@ -347,18 +349,117 @@ template <int D, int VB, bool FULL>
 __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int n, uint8_t* dst,
                                          int r0, const Lane<D>& hf) {
   constexpr int STEP = Lane<D>::STEP;
+  constexpr int R = 2;
 #pragma unroll 1
-  for (int t4 = hf.t0; t4 < BLOCK; t4 += 4 * STEP) {
-    Raw8<VB> raw[4];
+  for (int t4 = hf.t0; t4 < BLOCK; t4 += R * STEP) {
+    Raw8<VB> raw[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
       if (FULL || t4 + i * STEP < n) raw[i].load(vp + (t4 + i * STEP) * stride, hf.g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       const int t = t4 + i * STEP;
       uint32_t w[4] = {0, 0, 0, 0};
       if (FULL || t < n) unpack8w<VB, false>(raw[i], w);
-      *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// The loop of an unpacking warp: page `warp & 3` of every tile, its K or its V part.
+template <int D, bool ASYM, bool IS_K>
+__device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& A, uint8_t* smem,
+                                            TMisc& M, uint32_t out_full, uint32_t out_empty,
+                                            uint32_t raw_full, int warp, int lane) {
+  using Cfg = TCfg<D>;
+  const uint32_t raw_empty = raw_full + 8 * RAW_MAX;
+  volatile int* stop = &M.stop;
+  Walk w;
+  w.init(M, A.n_seqs, A.grid);
+  const int kmax = max(2, st.kmax[A.layer]);
+  const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
+  const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
+  const int pg = warp & 3;  // page of the tile
+  const Lane<D> hf(lane);
+  const int r0 = pg * BLOCK;
+  int rs = 0, sg = 0;
+  uint32_t rph = 0, eph = 1;
+  bool ok = true;
+  while (ok && w.next(M, st.G, st.Hkv)) {
+    for (int i = w.s; i < w.e; ++i) {
+      const bool drafts = i == w.nt - 1;
+      ok = ok && warp_wait(out_empty + 8 * sg, eph, stop);
+      if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+      if (!ok) break;
+      uint8_t* dst = IS_K ? smem + sg * Cfg::KSTAGE : smem + Cfg::V_OFF + sg * Cfg::OPND;
+      if (drafts) {  // raw rows of the drafted nodes
+        const int n = min(BLOCK, max(0, w.cnt - BLOCK * pg));
+        const size_t at = (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
+        const int64_t stride = (int64_t)st.Hkv * D * 2;
+        if constexpr (IS_K) {
+          if (pg == 0 && lane == 0) M.has_lo[sg] = 0;
+          unpack_k<D, 16, ASYM, false>(reinterpret_cast<const uint8_t*>(A.k + at), stride, n, dst,
+                                       false, r0, hf);
+        } else {
+          unpack_v<D, 16, false>(reinterpret_cast<const uint8_t*>(A.v + at), stride, n, dst, r0,
+                                 hf);
+        }
+      } else {
+        const int32_t e = M.ent[rs][pg];
+        const int n = e == -1 ? 0 : min(BLOCK, w.len - (i * TPAGES + pg) * BLOCK);
+        const int fmt = entry_fmt(e), kb = bits_of_code(fmt >> 2);
+        const uint8_t* page = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
+        const int v_off = k_part_bytes(kb, D, ASYM);
+        if constexpr (IS_K) {
+          const bool lo = M.raw_lo[rs] != 0;
+          if (pg == 0 && lane == 0) M.has_lo[sg] = lo;
+          if (n == BLOCK) {
+            switch (kb) {
+              case 2: unpack_k<D, 2, ASYM, true>(page, D / 4, n, dst, lo, r0, hf); break;
+              case 4: unpack_k<D, 4, ASYM, true>(page, D / 2, n, dst, lo, r0, hf); break;
+              case 8: unpack_k<D, 8, ASYM, true>(page, D, n, dst, lo, r0, hf); break;
+              default: unpack_k<D, 16, ASYM, true>(page, 2 * D, n, dst, lo, r0, hf); break;
+            }
+          } else if (n > 0) {  // the open block: raw rows, read from memory
+            const __half* stg =
+                st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
+            unpack_k<D, 16, ASYM, false>(reinterpret_cast<const uint8_t*>(stg), 2 * D, n, dst, lo,
+                                         r0, hf);
+          }
+        } else if (n == BLOCK) {
+          switch (A.vb) {
+            case 2: unpack_v<D, 2, true>(page + v_off, D / 4, n, dst, r0, hf); break;
+            case 4: unpack_v<D, 4, true>(page + v_off, D / 2, n, dst, r0, hf); break;
+            case 8: unpack_v<D, 8, true>(page + v_off, D, n, dst, r0, hf); break;
+            default: unpack_v<D, 16, true>(page + v_off, 2 * D, n, dst, r0, hf); break;
+          }
+        } else {  // the open block's rows in its page in memory, or none (zeros)
+          const uint8_t* vp = n > 0 ? st.pool_base[fmt] + v_off +
+                                          (size_t)entry_idx(e) * st.pool_page_bytes[fmt]
+                                    : nullptr;
+          switch (A.vb) {
+            case 2: unpack_v<D, 2, false>(vp, D / 4, n, dst, r0, hf); break;
+            case 4: unpack_v<D, 4, false>(vp, D / 2, n, dst, r0, hf); break;
+            case 8: unpack_v<D, 8, false>(vp, D, n, dst, r0, hf); break;
+            default: unpack_v<D, 16, false>(vp, 2 * D, n, dst, r0, hf); break;
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(out_full + 8 * sg);
+        if (!drafts) bar_arrive(raw_empty + 8 * rs);
+      }
+      if (++sg == (IS_K ? KST : VST)) {
+        sg = 0;
+        eph ^= 1;
+      }
+      if (!drafts && ++rs == nraw) {
+        rs = 0;
+        rph ^= 1;
+      }
     }
   }
 }
@@ -390,17 +491,17 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   }
   if (tid == 0) {
     for (int i = 0; i < KST; ++i) {
-      bar_init(k_full + 8 * i, DW);
+      bar_init(k_full + 8 * i, TPAGES);
       bar_init(k_empty + 8 * i, 1);
     }
     for (int i = 0; i < VST; ++i) {
-      bar_init(v_full + 8 * i, DW);
+      bar_init(v_full + 8 * i, TPAGES);
       bar_init(v_empty + 8 * i, 1);
-      bar_init(sc_full + 8 * i, TPAGES);
+      bar_init(sc_full + 8 * i, 1);
     }
     for (int i = 0; i < RAW_MAX; ++i) {
       bar_init(raw_full + 8 * i, 1);
-      bar_init(raw_empty + 8 * i, DW);
+      bar_init(raw_empty + 8 * i, 2 * TPAGES + 1);
     }
     for (int t = 0; t < 2; ++t) {
       bar_init(q_full + 8 * t, 4);
@@ -411,7 +512,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     M.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tmem_alloc(smem_u32(&M.tmem), 512);
+  if (warp == 16) tmem_alloc(smem_u32(&M.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
@@ -438,7 +539,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   }
   __syncthreads();
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_OTHER));
     Walk w;
     w.init(M, A.n_seqs, A.grid);
@@ -446,7 +547,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     const int kmax = max(2, st.kmax[A.layer]);
     const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
     const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-    if (warp == 13) {
+    if (warp == 17) {
       // ---- page copies ---------------------------------------------------------------
       int rs = 0;
       uint32_t ph = 1;
@@ -472,6 +573,10 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             else if (b < sealed) bytes = (uint32_t)st.pool_page_bytes[entry_fmt(e)];
           }
           if (lane < TPAGES) M.ent[rs][lane] = b < nblk ? e : -1;
+          const bool sealed_lo = lane < TPAGES && e != -1 && b < sealed &&
+                                 (entry_fmt(e) >> 2) < 3 && (ASYM || (entry_fmt(e) >> 2) > 0);
+          const bool lo = __any_sync(0xffffffffu, sealed_lo);
+          if (lane == 0) M.raw_lo[rs] = lo;
           uint32_t all = bytes;
           all += __shfl_xor_sync(0xffffffffu, all, 1);
           all += __shfl_xor_sync(0xffffffffu, all, 2);
@@ -493,7 +598,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
         }
       }
-    } else if (warp == 12) {
+    } else if (warp == 16) {
       // ---- products ------------------------------------------------------------------
       constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false), ID_O = idesc_f16(TM_ROWS, D, true);
       int ks = 0, vs = 0;
@@ -504,17 +609,14 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         const uint32_t d = uniform(tm + 256 * t + 64), q = uniform(tm + 256 * t);
         const bool lo = uniform(M.has_lo[sg]) != 0;
         if (elect()) {
+          // sub-tiles of 64 channels: those of hi, then those of lo
+          const int n = (lo ? 2 : 1) * (D / 64);
+#pragma unroll 1
+          for (int x = 0; x < n; ++x)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ts(d, q + 8 * k,
-                   desc_sw128(base + (k / 4) * Cfg::SUBT + (k % 4) * 32, 16, 1024), ID_S, k > 0);
-          if (lo) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ts(d, q + 8 * k,
-                     desc_sw128(base + Cfg::OPND + (k / 4) * Cfg::SUBT + (k % 4) * 32, 16, 1024),
-                     ID_S, true);
-          }
+            for (int k = 0; k < 4; ++k)
+              mma_ts(d, q + (x & (D / 64 - 1)) * 32 + 8 * k,
+                     desc_sw128(base + x * Cfg::SUBT + k * 32, 16, 1024), ID_S, x > 0 || k > 0);
           mma_commit(s_full + 8 * t);
         }
         __syncwarp();
@@ -604,140 +706,71 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
         }
       }
-    }
-  } else if (warp >= 8) {
-    // ---- unpacking -------------------------------------------------------------------
-    Walk w;
-    w.init(M, A.n_seqs, A.grid);
-    const int kmax = max(2, st.kmax[A.layer]);
-    const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
-    const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-    const int pg = warp - 8;  // page of the tile
-    const Lane<D> hf(lane);
-    const int r0 = pg * BLOCK;
-    int rs = 0, ks = 0, vs = 0;
-    uint32_t rph = 0, keph = 1, veph = 1;
-    bool ok = true;
-    while (ok && w.next(M, st.G, st.Hkv)) {
-      const __half* stg = st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
-      for (int i = w.s; i < w.e && ok; ++i) {
-        const bool drafts = i == w.nt - 1;
-        if (!drafts) ok = warp_wait(raw_full + 8 * rs, rph, stop);
-        // Where the page's rows are, how many hold tokens, and whether the tile needs lo.
-        int kb = 16, vb = A.vb, n = 0;
-        bool want_lo = false, full = false;
-        const uint8_t *kp = nullptr, *vp = nullptr;
-        int64_t kst = 2 * D, vst = D * vb / 8;
-        const int raw = Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
-        int rawv = raw;
-        if (drafts) {
-          n = min(BLOCK, max(0, w.cnt - BLOCK * pg));
-          const size_t at = (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
-          kp = reinterpret_cast<const uint8_t*>(A.k + at);
-          vp = reinterpret_cast<const uint8_t*>(A.v + at);
-          vb = 16;
-          kst = vst = (int64_t)st.Hkv * D * 2;
-        } else if (ok) {
-          const int4 ent = *reinterpret_cast<const int4*>(M.ent[rs]);
-          const int32_t es[TPAGES] = {ent.x, ent.y, ent.z, ent.w};
-          int32_t e = -1;
+    } else if (warp == 18) {
+      // ---- V scales and which tokens there are, two tokens a lane -------------------
+      int rs = 0, vs = 0;
+      uint32_t rph = 0, eph = 1;
+      bool ok = true;
+      while (ok && w.next(M, st.G, st.Hkv)) {
+        for (int i = w.s; i < w.e; ++i) {
+          const bool drafts = i == w.nt - 1;
+          ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
+          if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+          if (!ok) break;
+          int n = drafts ? min(TN, w.cnt) : min(TN, w.len - i * TN);  // tokens of the tile
 #pragma unroll
-          for (int x = 0; x < TPAGES; ++x) {
-            const int b = bits_of_code(entry_fmt(es[x]) >> 2);
-            if (es[x] != -1 && (i * TPAGES + x + 1) * BLOCK <= w.len)
-              want_lo |= b < 16 && (ASYM || b > 2);
-            if (x == pg) e = es[x];
-          }
-          n = e == -1 ? 0 : min(BLOCK, w.len - (i * TPAGES + pg) * BLOCK);
-          if (n > 0) {
-            const int fmt = entry_fmt(e), pkb = bits_of_code(fmt >> 2);
-            rawv = raw + k_part_bytes(pkb, D, ASYM);
-            full = n == BLOCK;
-            if (full) {
-              kb = pkb;
-            } else {  // the open block: raw K rows, V in the page, both read from memory
-              kp = reinterpret_cast<const uint8_t*>(stg);
-              vp = st.pool_base[fmt] + (size_t)entry_idx(e) * st.pool_page_bytes[fmt] +
-                   k_part_bytes(pkb, D, ASYM);
+          for (int u = 0; u < 2; ++u) {
+            const int tok = lane + 32 * u, pg = tok / BLOCK, r = tok % BLOCK;
+            float s = 1.f, zv = 0.f;  // (rows of scale 0 hold zero codes only: any scale does)
+            bool there = tok < n;
+            if (!drafts) {
+              const int32_t e = M.ent[rs][pg];
+              there = there && e != -1;
+              if (there && A.vb < 16) {
+                const int fmt = entry_fmt(e);
+                const int off =
+                    k_part_bytes(bits_of_code(fmt >> 2), D, ASYM) + BLOCK * D * A.vb / 8;
+                const __half* sp;
+                if ((pg + 1) * BLOCK <= n)
+                  sp = reinterpret_cast<const __half*>(smem + Cfg::RAW_OFF + off +
+                                                       (rs * TPAGES + pg) * page_room);
+                else  // the open block
+                  sp = reinterpret_cast<const __half*>(
+                      st.pool_base[fmt] + off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt]);
+                s = __half2float(sp[r]);
+                if (ASYM)
+                  zv = fmaf(s, (float)(1 << (A.vb - 1)), __half2float(sp[BLOCK + r]));
+                if (s == 0.f) s = 1.f;
+              }
             }
+            const float inv = __fdividef(1.f, s);
+            M.lsv[vs][tok] = __log2f(s);
+            M.rsv[vs][tok] = inv;
+            if (ASYM) M.zsv[vs][tok] = zv * inv;
+            const uint32_t bits = __ballot_sync(0xffffffffu, there);
+            if (lane == 0) reinterpret_cast<uint32_t*>(M.valid[vs])[u] = bits;
           }
-        }
-        // Scales first: softmax needs them with the scores.
-        ok = ok && warp_wait(v_empty + 8 * vs, veph, stop);
-        if (!ok) break;
-        if (lane < BLOCK) {  // token `lane` (rows of scale 0 hold zero codes only)
-          float s = 1.f, zv = 0.f;
-          if (vb < 16 && lane < n) {
-            const __half* sp = full
-                ? reinterpret_cast<const __half*>(smem + rawv + BLOCK * D * vb / 8)
-                : reinterpret_cast<const __half*>(vp + BLOCK * D * vb / 8);
-            s = __half2float(sp[lane]);
-            if (ASYM) zv = fmaf(s, (float)(1 << (vb - 1)), __half2float(sp[BLOCK + lane]));
-            if (s == 0.f) s = 1.f;
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(sc_full + 8 * vs);
+            if (!drafts) bar_arrive(raw_empty + 8 * rs);
           }
-          const float r = __fdividef(1.f, s);
-          M.lsv[vs][r0 + lane] = __log2f(s);
-          M.rsv[vs][r0 + lane] = r;
-          if (ASYM) M.zsv[vs][r0 + lane] = zv * r;
-        }
-        if (lane == 0) M.valid[vs][pg] = (uint16_t)((1u << n) - 1);
-        __syncwarp();
-        if (lane == 0) bar_arrive(sc_full + 8 * vs);
-        ok = warp_wait(k_empty + 8 * ks, keph, stop);
-        if (!ok) break;
-        uint8_t* hi = smem + ks * Cfg::KSTAGE;
-        if (full) {
-          const uint8_t* sp = smem + raw;
-          switch (kb) {
-            case 2: unpack_k<D, 2, ASYM, true>(sp, D / 4, n, hi, want_lo, r0, hf); break;
-            case 4: unpack_k<D, 4, ASYM, true>(sp, D / 2, n, hi, want_lo, r0, hf); break;
-            case 8: unpack_k<D, 8, ASYM, true>(sp, D, n, hi, want_lo, r0, hf); break;
-            default: unpack_k<D, 16, ASYM, true>(sp, 2 * D, n, hi, want_lo, r0, hf); break;
+          if (++vs == VST) {
+            vs = 0;
+            eph ^= 1;
           }
-        } else if (n > 0) {
-          unpack_k<D, 16, ASYM, false>(kp, kst, n, hi, want_lo, r0, hf);
-        }
-        if (pg == 0 && lane == 0) M.has_lo[ks] = want_lo;
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(k_full + 8 * ks);
-        uint8_t* vt = smem + Cfg::V_OFF + vs * Cfg::OPND;
-        if (full) {
-          const uint8_t* sp = smem + rawv;
-          switch (vb) {
-            case 2: unpack_v<D, 2, true>(sp, D / 4, n, vt, r0, hf); break;
-            case 4: unpack_v<D, 4, true>(sp, D / 2, n, vt, r0, hf); break;
-            case 8: unpack_v<D, 8, true>(sp, D, n, vt, r0, hf); break;
-            default: unpack_v<D, 16, true>(sp, 2 * D, n, vt, r0, hf); break;
+          if (!drafts && ++rs == nraw) {
+            rs = 0;
+            rph ^= 1;
           }
-        } else {
-          switch (vb) {
-            case 2: unpack_v<D, 2, false>(vp, vst, n, vt, r0, hf); break;
-            case 4: unpack_v<D, 4, false>(vp, vst, n, vt, r0, hf); break;
-            case 8: unpack_v<D, 8, false>(vp, vst, n, vt, r0, hf); break;
-            default: unpack_v<D, 16, false>(vp, vst, n, vt, r0, hf); break;
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(v_full + 8 * vs);
-          if (!drafts) bar_arrive(raw_empty + 8 * rs);
-        }
-        if (++ks == KST) {
-          ks = 0;
-          keph ^= 1;
-        }
-        if (++vs == VST) {
-          vs = 0;
-          veph ^= 1;
-        }
-        if (!drafts && ++rs == nraw) {
-          rs = 0;
-          rph ^= 1;
         }
       }
     }
+  } else if (warp >= 8) {
+    // ---- unpacking -------------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_UNPACK));
+    if (warp < 12) unpack_role<D, ASYM, true>(st, A, smem, M, k_full, k_empty, raw_full, warp, lane);
+    else unpack_role<D, ASYM, false>(st, A, smem, M, v_full, v_empty, raw_full, warp, lane);
   } else {
     // ---- softmax: thread = row ---------------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TREGS_SOFTMAX));
@@ -759,15 +792,15 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       const size_t qrow = (((size_t)w.z * A.m + node) * st.Hq + w.h * st.G + (mine ? gh : 0)) * D;
       const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without rows
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32];
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint4 v = mine ? __ldg(reinterpret_cast<const uint4*>(A.q + qrow) + 8 * c + u)
+        for (int u = 0; u < 4; ++u) {
+          const uint4 v = mine ? __ldg(reinterpret_cast<const uint4*>(A.q + qrow) + 4 * c + u)
                                : make_uint4(0, 0, 0, 0);
           perm8(v, x + 4 * u);
         }
-        tmem_st32(tq + 32 * c, x);
+        tmem_st16(tq + 16 * c, x);
       }
       tmem_wait_st();
       fence_before();
@@ -802,87 +835,96 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         sph ^= 1;
         fence_after();
         if (!idle) {
-          uint32_t s[64];
-          tmem_ld32(ts, s);
-          tmem_ld32(ts + 32, s + 32);
+          const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
           const unsigned long long seen =
               *reinterpret_cast<const unsigned long long*>(M.valid[sg]) &
               (i == w.nt - 1 ? M.anc[par][node] : ~0ull);
-          tmem_wait_ld();
-          const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
-          uint64_t y[32];
-          const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]);
+          const bool part = __any_sync(0xffffffffu, seen != ~0ull);
+          // Scores are read from tensor memory twice, 32 columns at a time (short loops
+          // keep the roles' code within the instruction caches).
+          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            float x[32];
+            tmem_ld32(ts + 32 * hf, reinterpret_cast<uint32_t*>(x));
+            const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]) + 8 * hf;
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 a = lv[c];
-            const float* x = reinterpret_cast<const float*>(s) + 4 * c;
-            y[2 * c] = fma2(pack2(x[0], x[1]), sl2, a.x);
-            y[2 * c + 1] = fma2(pack2(x[2], x[3]), sl2, a.y);
-          }
-          if (__any_sync(0xffffffffu, seen != ~0ull)) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float a, b;
-              unpack2(y[c], a, b);
-              if (!(seen >> (2 * c) & 1)) a = -CUDART_INF_F;
-              if (!(seen >> (2 * c + 1) & 1)) b = -CUDART_INF_F;
-              y[c] = pack2(a, b);
+            for (int c = 0; c < 8; ++c) {  // x + log2 s
+              const ulonglong2 a = lv[c];
+              unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), sl2, a.x), x[4 * c], x[4 * c + 1]);
+              unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), sl2, a.y), x[4 * c + 2], x[4 * c + 3]);
             }
-          }
-          float mx = -CUDART_INF_F, my = -CUDART_INF_F;
+            if (part) {
+              const uint32_t bits = (uint32_t)(seen >> (32 * hf));
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a, b;
-            unpack2(y[c], a, b);
-            mx = fmaxf(mx, a);
-            my = fmaxf(my, b);
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1)) x[c] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
           }
-          mx = fmaxf(mx, my);
-          const bool move = mx > mref + SLACK;
+          const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool move = mnew > mref + SLACK;
           if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? ex2(mref - mx) : 1.f;
-            if (move) mref = mx;
+            const float f = move ? ex2(mref - mnew) : 1.f;
+            if (move) mref = mnew;
             if (done > 0) {  // O holds this stream's products up to the tile before
               ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
               if (!ok) break;
               fence_after();
               l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
               if (ASYM) z2 = fma2(z2, pack2(f, f), pack2(0.f, 0.f));
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t x[16];
-                tmem_ld16(to + 16 * c, x);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(to + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 16; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * f);
-                tmem_st16(to + 16 * c, x);
+                for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * f);
+                tmem_st16(to + c, v);
               }
             }
           }
           const uint64_t off = pack2(BOOST - mref, BOOST - mref);
-          const ulonglong2* rv = reinterpret_cast<const ulonglong2*>(M.rsv[sg]);
-          const ulonglong2* zv = reinterpret_cast<const ulonglong2*>(M.zsv[sg]);
-          uint32_t p[32];
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            float x[32];
+            tmem_ld32(ts + 32 * hf, reinterpret_cast<uint32_t*>(x));
+            const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]) + 8 * hf;
+            const ulonglong2* rv = reinterpret_cast<const ulonglong2*>(M.rsv[sg]) + 8 * hf;
+            const ulonglong2* zv = reinterpret_cast<const ulonglong2*>(M.zsv[sg]) + 8 * hf;
+            tmem_wait_ld();
+            if (part) {
+              const uint32_t bits = (uint32_t)(seen >> (32 * hf));
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 ra = rv[c];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float a, b;
-              unpack2(add2(y[2 * c + u], off), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              const uint64_t ab = pack2(a, b);
-              l2 = fma2(ab, u ? ra.y : ra.x, l2);
-              if (ASYM) {
-                const ulonglong2 za = zv[c];
-                z2 = fma2(ab, u ? za.y : za.x, z2);
-              }
-              const __half2 hh = __floats2half2_rn(a, b);
-              p[2 * c + u] = *reinterpret_cast<const uint32_t*>(&hh);
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1)) x[c] = -CUDART_INF_F;
             }
+            uint32_t p[16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const ulonglong2 la = lv[c], ra = rv[c];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                float a, b;
+                unpack2(fma2(pack2(x[4 * c + 2 * u], x[4 * c + 2 * u + 1]), sl2,
+                             add2(u ? la.y : la.x, off)),
+                        a, b);
+                a = ex2(a);
+                b = ex2(b);
+                const uint64_t ab = pack2(a, b);
+                l2 = fma2(ab, u ? ra.y : ra.x, l2);
+                if (ASYM) {
+                  const ulonglong2 za = zv[c];
+                  z2 = fma2(ab, u ? za.y : za.x, z2);
+                }
+                const __half2 hh = __floats2half2_rn(a, b);
+                p[2 * c + u] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+            }
+            tmem_st16(ts + 16 * hf, p);  // over scores already read
           }
-          tmem_st32(ts, p);
           tmem_wait_st();
         }
         fence_before();
@@ -966,7 +1008,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     if (!ok && lane == 0) set_error(st, EKV_ETIMEOUT);
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     fence_after();
     if (*stop) {
       if (lane == 0) set_error(st, EKV_ETIMEOUT);
