@@ -244,12 +244,12 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         const uint32_t a = sb + Cfg::Q_OFF + t * TILE;
         const uint32_t b = uniform(sb + Cfg::KV_OFF + ks * TILE);
         if (elect()) {
-#pragma unroll 1
-          for (int x = 0; x < NSUB; ++x)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss(tm + t * BM, desc_sw128(a + x * SUB + k * 32, 16, 1024),
-                     desc_sw128(b + x * SUB + k * 32, 16, 1024), ID_S, x > 0 || k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * SUB + (k % 4) * 32;
+            mma_ss(tm + t * BM, desc_sw128(a + off, 16, 1024), desc_sw128(b + off, 16, 1024), ID_S,
+                   k > 0);
+          }
           mma_commit(s_full + 8 * t);
         }
         __syncwarp();
@@ -258,12 +258,10 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         const uint32_t b = uniform(sb + Cfg::KV_OFF + vs * TILE);
         const bool acc = uniform(!first);
         if (elect()) {
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int k = 4 * x; k < 4 * x + 4; ++k)
-              mma_ts(tm + 256 + t * D, tm + t * BM + k * 8, desc_sw128(b + k * 2048, SUB, 1024),
-                     ID_O, acc || k > 0);
+          for (int k = 0; k < BM / 16; ++k)
+            mma_ts(tm + 256 + t * D, tm + t * BM + k * 8, desc_sw128(b + k * 2048, SUB, 1024), ID_O,
+                   acc || k > 0);
           mma_commit(o_done + 8 * t);
         }
         __syncwarp();
@@ -345,25 +343,23 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
         if (!ok) break;
         sph ^= 1;
         fence_after();
-        // Scores are read from tensor memory twice, 32 columns at a time: short loops keep
-        // the CTA's code small (unrolled over 128 columns the roles' code outgrows the
-        // instruction caches and every warp waits for its instructions).
-        const bool diag = j == nk - 1;
-        const int here = diag ? (warp & 3) + 1 : 4;  // chunks with an unmasked score
-        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-        for (int c = 0; c < here; ++c) {
-          float x[32];
-          tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(x));
-          tmem_wait_ld();
-          if (diag && c == here - 1) {
+        uint32_t s[128];
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              if (u > lane) x[u] = -CUDART_INF_F;
-          }
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+        float* x = reinterpret_cast<float*>(s);
+        if (j == nk - 1) {  // the diagonal tile
 #pragma unroll
-          for (int u = 0; u < 32; ++u) mx[u & 3] = fmaxf(mx[u & 3], x[u]);
+          for (int c = 0; c < 128; ++c)
+            if (c > row) x[c] = -CUDART_INF_F;
         }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], fmaxf(x[c + 2 * u], x[c + 2 * u + 1]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[124 + u]);
         const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.sl;
         const bool move = j == 0 || mnew > mref + SLACK;
         if (j == 0) {
@@ -376,7 +372,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
           if (!ok) break;
           fence_after();
           l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
             tmem_ld32(to + 32 * c, r);
@@ -387,34 +383,19 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
           }
         }
         const uint64_t sl2 = pack2(A.sl, A.sl), mm = pack2(BOOST - mref, BOOST - mref);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
-          if (c < here) {
-            float x[32];
-            tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(x));
-            tmem_wait_ld();
-            if (diag && c == here - 1) {
+        uint32_t p[64];
 #pragma unroll
-              for (int u = 0; u < 32; ++u)
-                if (u > lane) x[u] = -CUDART_INF_F;
-            }
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              float a, b;
-              unpack2(fma2(pack2(x[2 * u], x[2 * u + 1]), sl2, mm), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              l2 = add2(l2, pack2(a, b));
-              const __half2 hh = __floats2half2_rn(a, b);
-              p[u] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 16; ++u) p[u] = 0;
-          }
-          tmem_st16(ts + 16 * c, p);  // over scores already read
+        for (int c = 0; c < 64; ++c) {
+          float a, b;
+          unpack2(fma2(pack2(x[2 * c], x[2 * c + 1]), sl2, mm), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          l2 = add2(l2, pack2(a, b));
+          const __half2 hh = __floats2half2_rn(a, b);
+          p[c] = *reinterpret_cast<const uint32_t*>(&hh);
         }
+        tmem_st32(ts, p);
+        tmem_st32(ts + 32, p + 32);
         tmem_wait_st();
         fence_before();
         __syncwarp();
@@ -430,7 +411,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
       const float inv = ok ? 1.f / (la + lb) : CUDART_NAN_F;
       const bool mine = i < tb.len[cur.z];
       __half* dst = A.o + (int64_t)(tb.start[cur.z] + (mine ? i : 0)) * A.os + (size_t)h * D;
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(to + 32 * c, r);

@@ -40,29 +40,26 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
-      "selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
 // Wait for the phase of the given parity; bounded.  Gives up (false) when the bound runs
-// out or another thread of the CTA already did; `stop` records it.
-constexpr int TC_WAIT_LIMIT = 1 << 22;
+// out (100,000 waits that the hardware may each hold for 20 us: 2 s) or another thread of
+// the CTA already did; `stop` records it.
+constexpr int TC_WAIT_LIMIT = 100000;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  if (bar_try(bar, parity)) return true;
+#pragma unroll 1
   for (int i = 0; i < TC_WAIT_LIMIT; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if ((i & 63) == 63 && *stop) return false;
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000)
+        : "memory");
+    if (done) return true;
+    if (*stop) return false;
   }
   *stop = 1;
   return false;
 }
-
 // The same for a whole warp, with one outcome.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, stop));

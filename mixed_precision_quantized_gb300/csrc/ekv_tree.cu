@@ -12,10 +12,11 @@
 // unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
 // tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
 //   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
-//   warps 8-11, 12-15  unpack the K and the V parts of a raw tile, a page a warp, into
-//                swizzled fp16 operand tiles: K as hi + lo (khat = code * scale = hi + lo
-//                exactly, two products; 2- and 16-bit K need hi alone), V as the bare
-//                codes (exact in fp16)
+//   warps 8-15   unpack the K (8, 9, 12, 13) and the V parts of a raw tile, a page a warp
+//                (K and V on different schedulers: less code for each), into swizzled
+//                fp16 operand tiles: K as hi + lo (khat = code * scale = hi + lo exactly,
+//                two products; 2- and 16-bit K need hi alone), V as the bare codes (exact
+//                in fp16)
 //   warp 18      the V scales of a tile, for softmax
 //   warp 16      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
 //   warps 0-3, 4-7  two softmax streams, one row a thread
@@ -47,9 +48,6 @@ constexpr int TM_ROWS = 128;      // rows of a row tile
 constexpr int TN = 64;            // tokens of a token tile
 constexpr int TPAGES = TN / BLOCK;
 constexpr int TT = 640;           // threads
-// 96 registers a thread at launch (65,536 / 640, in eights: 61,440 in all); softmax takes
-// 128, unpacking 80, the rest 64: 256 x 128 + 256 x 80 + 128 x 64.
-constexpr int TREGS_SOFTMAX = 128, TREGS_UNPACK = 80, TREGS_OTHER = 64;
 constexpr int TSEQS = 512;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
 constexpr int VST = 3;            // V operand tiles in flight (until their products are done)
@@ -64,6 +62,24 @@ struct TCfg {
   static constexpr int V_OFF = KST * KSTAGE;
   static constexpr int RAW_OFF = V_OFF + VST * OPND;
   static constexpr int MISC_OFF = RAW_OFF + RAW_BYTES;
+};
+
+// A segment: the token tiles s .. e-1 of one unit.
+struct TMisc;
+struct Seg {
+  int z, h, row0, nrt, s, e, nt, len, cnt;  // nrt: row tiles of the unit
+  int slot;  // of its partial
+  __device__ bool whole() const { return s == 0 && e == nt; }
+  // Tokens of page pg of tile i (its raw tile in slot rs).
+  __device__ int tokens(int i, const TMisc& M, int rs, int pg) const;
+};
+
+// Walks a CTA's segments in order.  Every warp has a walk of its own in shared memory, so
+// that the (long) step is one out-of-line function and takes no registers of the roles.
+struct Walk {
+  int64_t lo, hi, a;  // run, cost offset of the next unit
+  int z, unit, nunits, nt, cost, len, cnt;
+  Seg seg;
 };
 
 struct TMisc {
@@ -82,6 +98,7 @@ struct TMisc {
   int32_t raw_lo[RAW_MAX];                   // whether its K needs the lo products
   float ml[2][3][TM_ROWS];      // (m, l, z) of the two streams
   alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 4 * 2];
+  Walk walk[TT / 32];
   int stop;
   uint32_t tmem;
 };
@@ -121,61 +138,75 @@ __host__ __device__ inline void unit_part(int64_t a, int nt, int cost, int64_t l
   e = (int)(y < nt ? y : nt);
 }
 
-// A CTA's segments in order, the same in every role.
-struct Walk {
-  int64_t lo, hi, a;       // run, cost offset of the unit
-  int z, unit, nunits, nt, cost;
-  int h, row0, nrt, rows, s, e, len, cnt, n;
-  __device__ void init(const TMisc& M, int n_seqs, int grid) {
-    n = n_seqs;
-    const int64_t total = M.pre[n_seqs];
-    lo = run_start(total, blockIdx.x, grid);
-    hi = run_start(total, blockIdx.x + 1, grid);
-    int p = 0, q = n_seqs;  // the last sequence that starts at or before lo
-    while (q - p > 1) {
-      const int mid = (p + q) / 2;
-      if (M.pre[mid] <= lo) p = mid;
-      else q = mid;
-    }
-    z = p - 1;
-    unit = nunits = 0;
+__device__ __forceinline__ int Seg::tokens(int i, const TMisc& M, int rs, int pg) const {
+  if (i == nt - 1) return min(BLOCK, max(0, cnt - BLOCK * pg));
+  return M.ent[rs][pg] == -1 ? 0 : max(0, min(BLOCK, len - (i * TPAGES + pg) * BLOCK));
+}
+
+// First step: the sequence that holds the run's start.
+__device__ __noinline__ void walk_init(Walk* w, const TMisc& M, int n_seqs, int grid) {
+  const int64_t total = M.pre[n_seqs];
+  w->lo = run_start(total, blockIdx.x, grid);
+  w->hi = run_start(total, blockIdx.x + 1, grid);
+  int p = 0, q = n_seqs;  // the last sequence that starts at or before the run
+  while (q - p > 1) {
+    const int mid = (p + q) / 2;
+    if (M.pre[mid] <= w->lo) p = mid;
+    else q = mid;
   }
-  __device__ bool next(const TMisc& M, int G, int Hkv) {
-    while (true) {
-      if (unit >= nunits) {
-        if (++z >= n || M.pre[z] >= hi) return false;
-        len = M.len[z];
-        cnt = M.cnt[z];
-        const int r = rows_of(cnt, G);
-        nunits = cnt > 0 ? Hkv * pairs_of(r) : 0;
-        nt = tiles_of(len);
-        cost = tile_cost(r);
-        a = M.pre[z];
-        unit = 0;
-        if (nunits && lo > a) {  // skip the units before the run
-          const int64_t skip = (lo - a) / ((int64_t)nt * cost);
-          unit = (int)(skip < nunits ? skip : nunits);
-          a += (int64_t)unit * nt * cost;
-        }
-        continue;
+  w->z = p - 1;
+  w->unit = w->nunits = 0;
+}
+// Step to the next segment (false: none).
+__device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int G, int Hkv) {
+  while (true) {
+    if (w->unit >= w->nunits) {
+      const int z = ++w->z;
+      if (z >= n_seqs || M.pre[z] >= w->hi) return false;
+      w->len = M.len[z];
+      w->cnt = M.cnt[z];
+      const int r = rows_of(w->cnt, G);
+      w->nunits = w->cnt > 0 ? Hkv * pairs_of(r) : 0;
+      w->nt = tiles_of(w->len);
+      w->cost = tile_cost(r);
+      w->a = M.pre[z];
+      w->unit = 0;
+      if (w->nunits && w->lo > w->a) {  // skip the units before the run
+        const int64_t skip = (w->lo - w->a) / ((int64_t)w->nt * w->cost);
+        w->unit = (int)(skip < w->nunits ? skip : w->nunits);
+        w->a += (int64_t)w->unit * w->nt * w->cost;
       }
-      if (a >= hi) return false;
-      unit_part(a, nt, cost, lo, hi, s, e);
-      const int np = pairs_of(rows_of(cnt, G));
-      h = unit / np;
-      row0 = unit % np * 2 * TM_ROWS;
-      rows = min(2 * TM_ROWS, rows_of(cnt, G) - row0);
-      nrt = rows > TM_ROWS ? 2 : 1;
-      begun_ = a;
-      a += (int64_t)nt * cost;
-      ++unit;
-      if (s < e) return true;
+      continue;
     }
+    const int64_t a = w->a;
+    if (a >= w->hi) return false;
+    Seg& g = w->seg;
+    unit_part(a, w->nt, w->cost, w->lo, w->hi, g.s, g.e);
+    const int rows = rows_of(w->cnt, G), np = pairs_of(rows);
+    g.z = w->z;
+    g.h = w->unit / np;
+    g.row0 = w->unit % np * 2 * TM_ROWS;
+    g.nrt = rows - g.row0 > TM_ROWS ? 2 : 1;
+    g.nt = w->nt;
+    g.len = w->len;
+    g.cnt = w->cnt;
+    g.slot = 2 * blockIdx.x + (w->lo > a ? 0 : 1);
+    w->a = a + (int64_t)w->nt * w->cost;
+    ++w->unit;
+    if (g.s < g.e) return true;
   }
-  int64_t begun_;          // cost offset of the segment's unit
-  __device__ bool whole() const { return s == 0 && e == nt; }
-  __device__ int part_slot() const { return 2 * blockIdx.x + (lo > begun_ ? 0 : 1); }
-};
+}
+// By a whole warp: its next segment.
+__device__ __forceinline__ bool next_seg(Walk* wk, const TMisc& M, const TreeArgs& A,
+                                         const DevState& st, int lane, Seg& w) {
+  int more = 0;
+  if (lane == 0) more = walk_step(wk, M, A.n_seqs, st.G, st.Hkv);
+  more = __shfl_sync(0xffffffffu, more, 0);
+  __syncwarp();
+  w = wk->seg;
+  __syncwarp();
+  return more != 0;
+}
 
 // ---- unpacking: 8 channels (group g) of one row as 4 words, in the order
 // (0,4) (1,5) (2,6) (3,7), which 4-bit words unpack to with one AND-OR a pair.  Q is
@@ -198,7 +229,11 @@ __device__ __forceinline__ uint32_t hmul(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t hneg(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t hfms(uint32_t a, uint32_t b, uint32_t c) {  // a b - c
+  const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b),
+                            __hneg2(*reinterpret_cast<__half2*>(&c)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ void perm8(const uint4& u, uint32_t* w) {
   w[0] = __byte_perm(u.x, u.z, 0x5410);
   w[1] = __byte_perm(u.x, u.z, 0x7632);
@@ -278,96 +313,110 @@ __device__ __forceinline__ void channel8(const uint8_t* arr, int g, uint32_t* w)
   }
 }
 
-template <int D>
-__device__ __forceinline__ uint32_t tile_at(int row, int g) {  // 16-byte chunk of a tile
-  return (g >> 3) * TCfg<D>::SUBT + row * 128 + (((g & 7) ^ (row & 7)) << 4);
-}
-
-// A warp unpacks a page: group g of rows t0, t0 + STEP, ... (lanes side by side over the
-// groups of a row).  FULL: every row holds a token; else rows from n on
-// do not (K left as it is, V zero).
+// A warp unpacks one page: lane (g, t0) takes group g of rows t0, t0 + STEP, ...; OFF[i] is
+// where its i-th 16-byte chunk goes in the operand tile (swizzled: chunk g of row r sits at
+// (g mod 8) xor (r mod 8); every 8 rows the pattern repeats 1024 bytes on).
 template <int D>
 struct Lane {
   static constexpr int GR = D / 8, STEP = 32 / GR;
   int g, t0;
-  __device__ Lane(int lane) : g(lane % GR), t0(lane / GR) {}
+  uint32_t off[4];
+  __device__ Lane(int lane) : g(lane % GR), t0(lane / GR) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = t0 + i * STEP;
+      off[i] = (g >> 3) * TCfg<D>::SUBT + row * 128 + (((g & 7) ^ (row & 7)) << 4);
+    }
+  }
 };
 
+// K rows at kp into dst (hi) and dst + OPND (lo).  FULL: all 16 rows hold tokens; else rows
+// from n on are left as they are.  `lo`: the tile's lo part is used (zero it where this
+// page needs none).
 template <int D, int KB, bool ASYM, bool FULL>
-__device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int n, uint8_t* hi,
-                                         bool want_lo, int r0, const Lane<D>& hf) {
+__device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int n, uint8_t* dst,
+                                         bool lo, const Lane<D>& ln) {
   constexpr int STEP = Lane<D>::STEP;
+  constexpr int R = KB < 8 && !ASYM ? 4 : 2;  // rows at once
+  constexpr bool HAS_LO = KB < 16 && (ASYM || KB > 2);
   uint32_t sc[4], zp[4];
   if constexpr (KB < 16) {
-    channel8<KB>(kp + BLOCK * D * KB / 8, hf.g, sc);
-    if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, hf.g, zp);
+    channel8<KB>(kp + BLOCK * D * KB / 8, ln.g, sc);
+    if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, ln.g, zp);
   }
-  constexpr int R = 2;  // rows at once
 #pragma unroll 1
-  for (int t4 = hf.t0; t4 < BLOCK; t4 += R * STEP) {
-    Raw8<KB> raw[R];
+  for (int c = 0; c < BLOCK; c += 4 * STEP) {
+    const uint8_t* row = kp + (c + ln.t0) * stride;
+    uint8_t* out = dst + c * 128;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (FULL || t4 + i * STEP < n) raw[i].load(kp + (t4 + i * STEP) * stride, hf.g);
+    for (int j = 0; j < 4; j += R) {
+      Raw8<KB> raw[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int t = t4 + i * STEP;
-      if (!FULL && t >= n) break;
-      uint32_t w[4], l[4] = {0, 0, 0, 0};
-      unpack8w<KB, ASYM>(raw[i], w);
-      if constexpr (KB < 16 && !ASYM) {
+      for (int i = 0; i < R; ++i)
+        if (FULL || c + ln.t0 + (j + i) * STEP < n) raw[i].load(row + (j + i) * STEP * stride, ln.g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t p = hmul(w[j], sc[j]);
-          if constexpr (KB > 2) l[j] = hfma(w[j], sc[j], hneg(p));  // exact residual
-          w[j] = p;
+      for (int i = 0; i < R; ++i) {
+        if (!FULL && c + ln.t0 + (j + i) * STEP >= n) continue;
+        uint32_t w[4], l[4] = {0, 0, 0, 0};
+        unpack8w<KB, ASYM>(raw[i], w);
+        if constexpr (KB < 16 && !ASYM) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t p = hmul(w[x], sc[x]);
+            if constexpr (KB > 2) l[x] = hfms(w[x], sc[x], p);  // the exact residual
+            w[x] = p;
+          }
+        } else if constexpr (KB < 16) {  // u s + z in fp32, then hi + lo
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 u = __half22float2(*reinterpret_cast<__half2*>(&w[x]));
+            const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[x]));
+            const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[x]));
+            const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
+            const __half2 p = __floats2half2_rn(a, b);
+            const float2 pf = __half22float2(p);
+            const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
+            w[x] = *reinterpret_cast<const uint32_t*>(&p);
+            l[x] = *reinterpret_cast<const uint32_t*>(&r);
+          }
         }
-      } else if constexpr (KB < 16) {  // u s + z in fp32, then hi + lo
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = __half22float2(*reinterpret_cast<__half2*>(&w[j]));
-          const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[j]));
-          const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[j]));
-          const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
-          const __half2 p = __floats2half2_rn(a, b);
-          const float2 pf = __half22float2(p);
-          const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
-          w[j] = *reinterpret_cast<const uint32_t*>(&p);
-          l[j] = *reinterpret_cast<const uint32_t*>(&r);
-        }
+        uint8_t* at = out + ln.off[j + i];
+        *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (HAS_LO || lo)
+          *reinterpret_cast<uint4*>(at + TCfg<D>::OPND) = make_uint4(l[0], l[1], l[2], l[3]);
       }
-      uint8_t* at = hi + tile_at<D>(r0 + t, hf.g);
-      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (want_lo)
-        *reinterpret_cast<uint4*>(at + TCfg<D>::OPND) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
-// V codes are signed for both quantizers: u s + z = (u - 2^(b-1)) s + (z + 2^(b-1) s), so
-// that the products P' q stay as small as the values.
-template <int D, int VB, bool FULL>
+// V rows at vp into dst; rows from n on become zero.  Codes are signed for both
+// quantizers: u s + z = (u - 2^(b-1)) s + (z + 2^(b-1) s), so that the products P' q stay
+// as small as the values.
+template <int D, int VB>
 __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int n, uint8_t* dst,
-                                         int r0, const Lane<D>& hf) {
+                                         const Lane<D>& ln) {
   constexpr int STEP = Lane<D>::STEP;
-  constexpr int R = 2;
+  constexpr int R = VB < 8 ? 4 : 2;
 #pragma unroll 1
-  for (int t4 = hf.t0; t4 < BLOCK; t4 += R * STEP) {
-    Raw8<VB> raw[R];
+  for (int c = 0; c < BLOCK; c += 4 * STEP) {
+    const uint8_t* row = vp + (c + ln.t0) * stride;
+    uint8_t* out = dst + c * 128;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (FULL || t4 + i * STEP < n) raw[i].load(vp + (t4 + i * STEP) * stride, hf.g);
+    for (int j = 0; j < 4; j += R) {
+      Raw8<VB> raw[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int t = t4 + i * STEP;
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (FULL || t < n) unpack8w<VB, false>(raw[i], w);
-      *reinterpret_cast<uint4*>(dst + tile_at<D>(r0 + t, hf.g)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < R; ++i)
+        if (c + ln.t0 + (j + i) * STEP < n) raw[i].load(row + (j + i) * STEP * stride, ln.g);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (c + ln.t0 + (j + i) * STEP < n) unpack8w<VB, false>(raw[i], w);
+        *reinterpret_cast<uint4*>(out + ln.off[j + i]) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
 }
 
-// The loop of an unpacking warp: page `warp & 3` of every tile, its K or its V part.
+// The loop of an unpacking warp: one page of every tile, its K or its V part.
 template <int D, bool ASYM, bool IS_K>
 __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& A, uint8_t* smem,
                                             TMisc& M, uint32_t out_full, uint32_t out_empty,
@@ -375,75 +424,63 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
   using Cfg = TCfg<D>;
   const uint32_t raw_empty = raw_full + 8 * RAW_MAX;
   volatile int* stop = &M.stop;
-  Walk w;
-  w.init(M, A.n_seqs, A.grid);
+  Seg w;
   const int kmax = max(2, st.kmax[A.layer]);
   const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
   const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-  const int pg = warp & 3;  // page of the tile
+  const int pg = (warp & 1) + (warp >> 1 & 2);  // page of the tile
   const Lane<D> hf(lane);
-  const int r0 = pg * BLOCK;
   int rs = 0, sg = 0;
   uint32_t rph = 0, eph = 1;
   bool ok = true;
-  while (ok && w.next(M, st.G, st.Hkv)) {
+  while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
     for (int i = w.s; i < w.e; ++i) {
       const bool drafts = i == w.nt - 1;
       ok = ok && warp_wait(out_empty + 8 * sg, eph, stop);
       if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
       if (!ok) break;
-      uint8_t* dst = IS_K ? smem + sg * Cfg::KSTAGE : smem + Cfg::V_OFF + sg * Cfg::OPND;
-      if (drafts) {  // raw rows of the drafted nodes
-        const int n = min(BLOCK, max(0, w.cnt - BLOCK * pg));
-        const size_t at = (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
-        const int64_t stride = (int64_t)st.Hkv * D * 2;
-        if constexpr (IS_K) {
-          if (pg == 0 && lane == 0) M.has_lo[sg] = 0;
-          unpack_k<D, 16, ASYM, false>(reinterpret_cast<const uint8_t*>(A.k + at), stride, n, dst,
-                                       false, r0, hf);
-        } else {
-          unpack_v<D, 16, false>(reinterpret_cast<const uint8_t*>(A.v + at), stride, n, dst, r0,
-                                 hf);
+      uint8_t* dst = smem + (IS_K ? sg * Cfg::KSTAGE : Cfg::V_OFF + sg * Cfg::OPND) + pg * BLOCK * 128;
+      // Where the part's rows are and how many hold tokens: in the raw tile; the open
+      // block's K in the staging rows and V in its page, in memory; the drafts as given.
+      const int n = w.tokens(i, M, rs, pg);
+      const int32_t e = drafts ? -1 : M.ent[rs][pg];
+      const int kb = bits_of_code(entry_fmt(e) >> 2);
+      if constexpr (IS_K) {
+        const bool lo = !drafts && M.raw_lo[rs] != 0;
+        if (pg == 0 && lane == 0) M.has_lo[sg] = lo;
+        if (n == BLOCK && !drafts) {
+          const uint8_t* page = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
+          switch (kb) {
+            case 2: unpack_k<D, 2, ASYM, true>(page, D / 4, n, dst, lo, hf); break;
+            case 4: unpack_k<D, 4, ASYM, true>(page, D / 2, n, dst, lo, hf); break;
+            case 8: unpack_k<D, 8, ASYM, true>(page, D, n, dst, lo, hf); break;
+            default: unpack_k<D, 16, ASYM, true>(page, 2 * D, n, dst, lo, hf); break;
+          }
+        } else if (n > 0) {
+          const __half* kp =
+              drafts ? A.k + (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D
+                     : st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
+          unpack_k<D, 16, ASYM, false>(reinterpret_cast<const uint8_t*>(kp),
+                                       2 * D * (drafts ? (int64_t)st.Hkv : 1), n, dst, lo, hf);
         }
       } else {
-        const int32_t e = M.ent[rs][pg];
-        const int n = e == -1 ? 0 : min(BLOCK, w.len - (i * TPAGES + pg) * BLOCK);
-        const int fmt = entry_fmt(e), kb = bits_of_code(fmt >> 2);
-        const uint8_t* page = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
-        const int v_off = k_part_bytes(kb, D, ASYM);
-        if constexpr (IS_K) {
-          const bool lo = M.raw_lo[rs] != 0;
-          if (pg == 0 && lane == 0) M.has_lo[sg] = lo;
-          if (n == BLOCK) {
-            switch (kb) {
-              case 2: unpack_k<D, 2, ASYM, true>(page, D / 4, n, dst, lo, r0, hf); break;
-              case 4: unpack_k<D, 4, ASYM, true>(page, D / 2, n, dst, lo, r0, hf); break;
-              case 8: unpack_k<D, 8, ASYM, true>(page, D, n, dst, lo, r0, hf); break;
-              default: unpack_k<D, 16, ASYM, true>(page, 2 * D, n, dst, lo, r0, hf); break;
-            }
-          } else if (n > 0) {  // the open block: raw rows, read from memory
-            const __half* stg =
-                st.staging + lsh_index(st, A.layer, M.slot[w.z], w.h) * (BLOCK * D);
-            unpack_k<D, 16, ASYM, false>(reinterpret_cast<const uint8_t*>(stg), 2 * D, n, dst, lo,
-                                         r0, hf);
-          }
-        } else if (n == BLOCK) {
-          switch (A.vb) {
-            case 2: unpack_v<D, 2, true>(page + v_off, D / 4, n, dst, r0, hf); break;
-            case 4: unpack_v<D, 4, true>(page + v_off, D / 2, n, dst, r0, hf); break;
-            case 8: unpack_v<D, 8, true>(page + v_off, D, n, dst, r0, hf); break;
-            default: unpack_v<D, 16, true>(page + v_off, 2 * D, n, dst, r0, hf); break;
-          }
-        } else {  // the open block's rows in its page in memory, or none (zeros)
-          const uint8_t* vp = n > 0 ? st.pool_base[fmt] + v_off +
-                                          (size_t)entry_idx(e) * st.pool_page_bytes[fmt]
-                                    : nullptr;
-          switch (A.vb) {
-            case 2: unpack_v<D, 2, false>(vp, D / 4, n, dst, r0, hf); break;
-            case 4: unpack_v<D, 4, false>(vp, D / 2, n, dst, r0, hf); break;
-            case 8: unpack_v<D, 8, false>(vp, D, n, dst, r0, hf); break;
-            default: unpack_v<D, 16, false>(vp, 2 * D, n, dst, r0, hf); break;
-          }
+        const int fmt = entry_fmt(e), v_off = k_part_bytes(kb, D, ASYM);
+        const uint8_t* vp = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room + v_off;
+        int64_t stride = D * A.vb / 8;
+        int vb = A.vb;
+        if (drafts) {
+          vp = reinterpret_cast<const uint8_t*>(
+              A.v + (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D);
+          stride = 2 * D * (int64_t)st.Hkv;
+          vb = 16;
+        } else if (n > 0 && n < BLOCK) {
+          vp = st.pool_base[fmt] + v_off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt];
+        }
+        switch (vb) {
+          case 2: unpack_v<D, 2>(vp, stride, n, dst, hf); break;
+          case 4: unpack_v<D, 4>(vp, stride, n, dst, hf); break;
+          case 8: unpack_v<D, 8>(vp, stride, n, dst, hf); break;
+          default: unpack_v<D, 16>(vp, stride, n, dst, hf); break;
         }
       }
       fence_async_smem();
@@ -538,11 +575,11 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       for (int z = lane; z <= A.n_seqs; z += 32) A.pre[z] = M.pre[z];
   }
   __syncthreads();
+  if (lane == 0) walk_init(&M.walk[warp], M, A.n_seqs, A.grid);
+  __syncwarp();
 
   if (warp >= 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_OTHER));
-    Walk w;
-    w.init(M, A.n_seqs, A.grid);
+    Seg w;
     // Raw tile: 4 pages, each sized for the widest page the layer has admitted.
     const int kmax = max(2, st.kmax[A.layer]);
     const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
@@ -552,7 +589,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       int rs = 0;
       uint32_t ph = 1;
       bool ok = true;
-      while (ok && w.next(M, st.G, st.Hkv)) {
+      while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
         const int32_t* bt = st.bt + lsh_index(st, A.layer, M.slot[w.z], w.h) * st.maxblk;
         const int nblk = (w.len + BLOCK - 1) / BLOCK, sealed = w.len / BLOCK;
         const int end = min(w.e, w.nt - 1);  // the drafts' tile has no pages
@@ -662,47 +699,29 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         bits ^= 1u << t;
         fence_after();
       };
-      while (ok && w.next(M, st.G, st.Hkv)) {
-        const int n = w.e - w.s;
+      while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
         wait_on(q_full, qph, 0);
         wait_on(q_full, qph, 1);
-        if (w.nrt == 2) {  // both streams take every tile
-          int kg = next_k();
-          if (!ok) break;
-          scores(0, kg);
-          scores(1, kg);
-          release(k_empty + 8 * kg);
-          for (int i = 0; i < n && ok; ++i) {
-            const int vg = next_v();
-            if (i + 1 < n) kg = next_k();
-            for (int t = 0; t < 2 && ok; ++t) {
-              wait_on(p_full, pph, t);
-              if (!ok) break;
-              values(t, vg, i == 0);
-              if (i + 1 < n) scores(t, kg);
-            }
-            if (!ok) break;
-            release(v_empty + 8 * vg);
-            if (i + 1 < n) release(k_empty + 8 * kg);
-          }
-        } else {  // the streams take turns
-          int kg = next_k();
-          if (!ok) break;
-          scores(0, kg);
-          release(k_empty + 8 * kg);
-          for (int i = 0; i < n && ok; ++i) {
-            const int t = i & 1;
-            if (i + 1 < n) {
-              kg = next_k();
-              if (!ok) break;
-              scores(t ^ 1, kg);
-              release(k_empty + 8 * kg);
-            }
-            const int vg = next_v();
+        // Scores x = 0, 1, ... go to stream x mod 2 and their products two steps later: two
+        // row tiles over each token tile, or one over token tiles in turn.
+        const bool two = w.nrt == 2;
+        const int n = (w.e - w.s) * (two ? 2 : 1);
+        int kg = 0, vg = 0;
+#pragma unroll 1
+        for (int x = 0; x < n + 2 && ok; ++x) {
+          const int t = x & 1;
+          if (x >= 2) {
+            if (!two || t == 0) vg = next_v();
             wait_on(p_full, pph, t);
             if (!ok) break;
-            values(t, vg, i < 2);
-            release(v_empty + 8 * vg);
+            values(t, vg, x < 4);
+            if (!two || t == 1) release(v_empty + 8 * vg);
+          }
+          if (x < n) {
+            if (!two || t == 0) kg = next_k();
+            if (!ok) break;
+            scores(t, kg);
+            if (!two || t == 1) release(k_empty + 8 * kg);
           }
         }
       }
@@ -711,7 +730,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       int rs = 0, vs = 0;
       uint32_t rph = 0, eph = 1;
       bool ok = true;
-      while (ok && w.next(M, st.G, st.Hkv)) {
+      while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
         for (int i = w.s; i < w.e; ++i) {
           const bool drafts = i == w.nt - 1;
           ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
@@ -768,14 +787,11 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     }
   } else if (warp >= 8) {
     // ---- unpacking -------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREGS_UNPACK));
-    if (warp < 12) unpack_role<D, ASYM, true>(st, A, smem, M, k_full, k_empty, raw_full, warp, lane);
+    if (!(warp & 2)) unpack_role<D, ASYM, true>(st, A, smem, M, k_full, k_empty, raw_full, warp, lane);
     else unpack_role<D, ASYM, false>(st, A, smem, M, v_full, v_empty, raw_full, warp, lane);
   } else {
     // ---- softmax: thread = row ---------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TREGS_SOFTMAX));
-    Walk w;
-    w.init(M, A.n_seqs, A.grid);
+    Seg w;
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t base = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tq = base + 256 * t, ts = tq + 64, to = tq + 128;
@@ -783,7 +799,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     int par = 0, tiles_before = 0;  // segment parity; tiles of the segments before
     bool ok = true;
     constexpr float SLACK = 8.f, BOOST = 7.f, NONE = -1e30f;
-    while (w.next(M, st.G, st.Hkv)) {
+    while (next_seg(&M.walk[warp], M, A, st, lane, w)) {
       // This thread's row: node and query head of the group.
       const bool split = w.nrt == 1;  // streams share the rows and halve the tiles
       const int r = w.row0 + (split ? row : t * TM_ROWS + row);
@@ -862,7 +878,8 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                 if (!(bits >> c & 1)) x[c] = -CUDART_INF_F;
             }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            for (int c = 0; c < 32; c += 2)
+              mx[c >> 1 & 3] = fmaxf(mx[c >> 1 & 3], fmaxf(x[c], x[c + 1]));
           }
           const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool move = mnew > mref + SLACK;
@@ -964,9 +981,9 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int rt = split ? 0 : t;
       float4* part = reinterpret_cast<float4*>(A.acc) +
-                     ((size_t)w.part_slot() * 2 + rt) * (D / 4) * TM_ROWS;
+                     ((size_t)w.slot * 2 + rt) * (D / 4) * TM_ROWS;
       if (!direct && mine && c0 == 0)
-        A.ml[((size_t)w.part_slot() * 2 + rt) * TM_ROWS + row] = make_float2(m, l);
+        A.ml[((size_t)w.slot * 2 + rt) * TM_ROWS + row] = make_float2(m, l);
 #pragma unroll 1
       for (int c = c0; c < c1; c += 16) {
         uint32_t x[16], x1[16];
