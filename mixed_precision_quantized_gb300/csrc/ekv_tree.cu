@@ -18,19 +18,23 @@
 //                two products; 2- and 16-bit K need hi alone), V as the bare codes (exact
 //                in fp16)
 //   warp 18      the V scales of a tile, for softmax
-//   warp 16      tcgen05.mma: S = Q K^T with Q in tensor memory, O += P V
-//   warps 0-3, 4-7  two softmax streams, one row a thread
-// With more than 128 rows the two streams are two row tiles over the same tokens; with
-// fewer they are the even and odd token tiles of the same rows, merged at the end
-// (each reads the other's accumulator in tensor memory).
+//   warps 16, 19 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
+//                their waits in one loop took longer than the products)
+//   warps 0-3, 4-7  softmax, one row a thread; the two groups take the even and the odd
+//                token tiles of a pair, for the same rows
+// What bounds it at few rows is the chain of waits from scores to probabilities to
+// products, ~2,500 cycles; so scores run up to two pairs ahead (four score buffers in
+// tensor memory), with one accumulator and one running reference for both groups: before
+// the exponentials of a pair a barrier with an OR over the 256 threads tells whether any
+// row's reference has to move, which is seldom.
 //
 // A token's V scale s multiplies its probability: P' = 2^(x + log2 s - m) in fp16, where
 // the reference m follows the largest x + log2 s, so the fp16 range is used well whatever
 // the scales; the row sum adds P' / s in fp32.  As in prompt attention m moves only for
 // a gain above 2^8, P' carries 2^7, and P' is the one value rounded to fp16.
 //
-// Work split: all (sequence, KV head, row pair) units laid end to end in cost order of
-// their tiles, cut into equal runs, one per CTA (one CTA an SM); a run may hold parts of
+// Work split: the token tiles of all (sequence, KV head, row tile) units laid end to end,
+// cut into equal runs, one per CTA (one CTA an SM); a run may hold parts of
 // several units.  A unit cut by run ends leaves fp32 partials (numerator, max, sum) in
 // the scratch, and a second small kernel merges them by log-sum-exp.  The cut depends on
 // the lengths only, so equal calls give equal bits.
@@ -50,8 +54,8 @@ constexpr int TPAGES = TN / BLOCK;
 constexpr int TT = 640;           // threads
 constexpr int TSEQS = 512;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
-constexpr int VST = 3;            // V operand tiles in flight (until their products are done)
-constexpr int RAW_BYTES = 96 * 1024;
+constexpr int VST = 4;            // V operand tiles in flight (until their products are done)
+constexpr int RAW_BYTES = 80 * 1024;
 constexpr int RAW_MAX = 8;        // raw tiles in flight at most
 
 template <int D>
@@ -67,7 +71,7 @@ struct TCfg {
 // A segment: the token tiles s .. e-1 of one unit.
 struct TMisc;
 struct Seg {
-  int z, h, row0, nrt, s, e, nt, len, cnt;  // nrt: row tiles of the unit
+  int z, h, row0, s, e, nt, len, cnt;
   int slot;  // of its partial
   __device__ bool whole() const { return s == 0 && e == nt; }
   // Tokens of page pg of tile i (its raw tile in slot rs).
@@ -77,13 +81,13 @@ struct Seg {
 // Walks a CTA's segments in order.  Every warp has a walk of its own in shared memory, so
 // that the (long) step is one out-of-line function and takes no registers of the roles.
 struct Walk {
-  int64_t lo, hi, a;  // run, cost offset of the next unit
-  int z, unit, nunits, nt, cost, len, cnt;
+  int64_t lo, hi, a;  // run, offset of the next unit
+  int z, unit, nunits, nt, len, cnt;
   Seg seg;
 };
 
 struct TMisc {
-  int64_t pre[TSEQS + 1];       // cost of the sequences before
+  int64_t pre[TSEQS + 1];       // tiles of the sequences before
   int32_t len[TSEQS];           // cached tokens
   int32_t slot[TSEQS];
   uint8_t cnt[TSEQS];           // nodes
@@ -96,8 +100,9 @@ struct TMisc {
   int32_t has_lo[KST];
   alignas(16) int32_t ent[RAW_MAX][TPAGES];  // page-table entries of a raw tile
   int32_t raw_lo[RAW_MAX];                   // whether its K needs the lo products
-  float ml[2][3][TM_ROWS];      // (m, l, z) of the two streams
-  alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 4 * 2];
+  float mx[2][TM_ROWS];         // row maxima of the two groups, then their (sum, z)
+  float lz[2][2][TM_ROWS];
+  alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 1 + 4 + 4 + 2];
   Walk walk[TT / 32];
   int stop;
   uint32_t tmem;
@@ -108,32 +113,26 @@ struct TreeArgs {
   const int32_t *slots, *n_nodes, *parents;
   const __half *q, *k, *v;
   __half* o;
-  float* acc;       // [2 grid][2 row tiles][D / 4][128] float4
-  float2* ml;       // [2 grid][2][128] (max, sum)
+  float* acc;       // [2 grid][D / 4][128] float4
+  float2* ml;       // [2 grid][128] (max, sum)
   int64_t* pre;     // [n_seqs + 1] for the merging kernel
   int grid;
 };
 
 __host__ __device__ inline int rows_of(int cnt, int G) { return cnt * G; }
-__host__ __device__ inline int pairs_of(int rows) {  // row-tile pairs
-  return (rows + 2 * TM_ROWS - 1) / (2 * TM_ROWS);
-}
-// Cost of one token tile: two row tiles take about 3/2 of the time of one (the pages
-// and their unpacking are shared).
-__host__ __device__ inline int tile_cost(int rows) { return rows > TM_ROWS ? 3 : 2; }
+__host__ __device__ inline int row_tiles(int rows) { return (rows + TM_ROWS - 1) / TM_ROWS; }
 __host__ __device__ inline int tiles_of(int len) { return (len + TN - 1) / TN + 1; }  // + drafts
-__host__ __device__ inline int64_t seq_cost(int len, int cnt, int G, int Hkv) {
+__host__ __device__ inline int64_t seq_tiles(int len, int cnt, int G, int Hkv) {
   const int r = rows_of(cnt, G);
-  return cnt > 0 ? (int64_t)Hkv * pairs_of(r) * tiles_of(len) * tile_cost(r) : 0;
+  return cnt > 0 ? (int64_t)Hkv * row_tiles(r) * tiles_of(len) : 0;
 }
 __host__ __device__ inline int64_t run_start(int64_t total, int c, int grid) {
   return total * c / grid;
 }
-// Tiles of a unit at cost offset a that lie in the run [lo, hi).
-__host__ __device__ inline void unit_part(int64_t a, int nt, int cost, int64_t lo, int64_t hi,
-                                          int& s, int& e) {
-  const int64_t x = lo > a ? (lo - a + cost - 1) / cost : 0;
-  const int64_t y = hi > a ? (hi - a + cost - 1) / cost : 0;
+// Tiles of a unit of nt tiles at offset a that lie in the run [lo, hi).
+__host__ __device__ inline void unit_part(int64_t a, int nt, int64_t lo, int64_t hi, int& s,
+                                          int& e) {
+  const int64_t x = lo > a ? lo - a : 0, y = hi > a ? hi - a : 0;
   s = (int)(x < nt ? x : nt);
   e = (int)(y < nt ? y : nt);
 }
@@ -166,32 +165,30 @@ __device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int 
       w->len = M.len[z];
       w->cnt = M.cnt[z];
       const int r = rows_of(w->cnt, G);
-      w->nunits = w->cnt > 0 ? Hkv * pairs_of(r) : 0;
+      w->nunits = w->cnt > 0 ? Hkv * row_tiles(r) : 0;
       w->nt = tiles_of(w->len);
-      w->cost = tile_cost(r);
       w->a = M.pre[z];
       w->unit = 0;
       if (w->nunits && w->lo > w->a) {  // skip the units before the run
-        const int64_t skip = (w->lo - w->a) / ((int64_t)w->nt * w->cost);
+        const int64_t skip = (w->lo - w->a) / w->nt;
         w->unit = (int)(skip < w->nunits ? skip : w->nunits);
-        w->a += (int64_t)w->unit * w->nt * w->cost;
+        w->a += (int64_t)w->unit * w->nt;
       }
       continue;
     }
     const int64_t a = w->a;
     if (a >= w->hi) return false;
     Seg& g = w->seg;
-    unit_part(a, w->nt, w->cost, w->lo, w->hi, g.s, g.e);
-    const int rows = rows_of(w->cnt, G), np = pairs_of(rows);
+    unit_part(a, w->nt, w->lo, w->hi, g.s, g.e);
+    const int nr = row_tiles(rows_of(w->cnt, G));
     g.z = w->z;
-    g.h = w->unit / np;
-    g.row0 = w->unit % np * 2 * TM_ROWS;
-    g.nrt = rows - g.row0 > TM_ROWS ? 2 : 1;
+    g.h = w->unit / nr;
+    g.row0 = w->unit % nr * TM_ROWS;
     g.nt = w->nt;
     g.len = w->len;
     g.cnt = w->cnt;
     g.slot = 2 * blockIdx.x + (w->lo > a ? 0 : 1);
-    w->a = a + (int64_t)w->nt * w->cost;
+    w->a = a + w->nt;
     ++w->unit;
     if (g.s < g.e) return true;
   }
@@ -353,7 +350,8 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
       Raw8<KB> raw[R];
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (FULL || c + ln.t0 + (j + i) * STEP < n) raw[i].load(row + (j + i) * STEP * stride, ln.g);
+        if (FULL || c + ln.t0 + (j + i) * STEP < n)
+          raw[i].load(row + (j + i) * STEP * stride, ln.g);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (!FULL && c + ln.t0 + (j + i) * STEP >= n) continue;
@@ -439,7 +437,8 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
       ok = ok && warp_wait(out_empty + 8 * sg, eph, stop);
       if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
       if (!ok) break;
-      uint8_t* dst = smem + (IS_K ? sg * Cfg::KSTAGE : Cfg::V_OFF + sg * Cfg::OPND) + pg * BLOCK * 128;
+      uint8_t* dst = smem + pg * BLOCK * 128 +
+                     (IS_K ? sg * Cfg::KSTAGE : Cfg::V_OFF + sg * Cfg::OPND);
       // Where the part's rows are and how many hold tokens: in the raw tile; the open
       // block's K in the staging rows and V in its page, in memory; the drafts as given.
       const int n = w.tokens(i, M, rs, pg);
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                  v_empty = v_full + 8 * VST, sc_full = v_empty + 8 * VST,
                  raw_full = sc_full + 8 * VST, raw_empty = raw_full + 8 * RAW_MAX,
                  q_full = raw_empty + 8 * RAW_MAX,
-                 s_full = q_full + 16, p_full = s_full + 16, o_done = p_full + 16;
+                 s_full = q_full + 8, p_full = s_full + 32, o_done = p_full + 32;
   volatile int* stop = &M.stop;
 
   for (int z = tid; z < A.n_seqs; z += TT) {
@@ -540,12 +539,12 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       bar_init(raw_full + 8 * i, 1);
       bar_init(raw_empty + 8 * i, 2 * TPAGES + 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      bar_init(q_full + 8 * t, 4);
-      bar_init(s_full + 8 * t, 1);
-      bar_init(p_full + 8 * t, 4);
-      bar_init(o_done + 8 * t, 1);
+    bar_init(q_full, 8);
+    for (int i = 0; i < 4; ++i) {  // [buffer][group]
+      bar_init(s_full + 8 * i, 1);
+      bar_init(p_full + 8 * i, 4);
     }
+    for (int i = 0; i < 2; ++i) bar_init(o_done + 8 * i, 1);
     M.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -553,13 +552,13 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   fence_before();
   __syncthreads();
   fence_after();
-  // Stream t at column 256 t: Q (D / 2 columns), S and P at 64, O at 128.
+  // Columns: Q at 0 (D / 2), O at 64 (D), score buffer b of group t at 256 + 128 b + 64 t.
   const uint32_t tm = uniform(M.tmem);
-  if (warp == 0) {             // prefix of the sequences' costs
+  if (warp == 0) {             // prefix of the sequences' tiles
     int64_t run = 0;
     for (int z0 = 0; z0 < A.n_seqs; z0 += 32) {
       const int z = z0 + lane;
-      const int64_t c = z < A.n_seqs ? seq_cost(M.len[z], M.cnt[z], st.G, st.Hkv) : 0;
+      const int64_t c = z < A.n_seqs ? seq_tiles(M.len[z], M.cnt[z], st.G, st.Hkv) : 0;
       int64_t x = c;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -636,93 +635,80 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         }
       }
     } else if (warp == 16) {
-      // ---- products ------------------------------------------------------------------
-      constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false), ID_O = idesc_f16(TM_ROWS, D, true);
-      int ks = 0, vs = 0;
-      uint32_t kph = 0, vph = 0, qph = 0, pph = 0;
+      // ---- scores of token tile x into buffer (x / 2) mod 2 of group x mod 2 -----------
+      constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false);
+      int sg = 0, buf = 0;
+      uint32_t kph = 0, qph = 0, oph = 3;  // a buffer's first scores wait for no product
       bool ok = true;
-      auto scores = [&](int t, int sg) {
-        const uint32_t base = uniform(sb + sg * Cfg::KSTAGE);
-        const uint32_t d = uniform(tm + 256 * t + 64), q = uniform(tm + 256 * t);
-        const bool lo = uniform(M.has_lo[sg]) != 0;
-        if (elect()) {
-          // sub-tiles of 64 channels: those of hi, then those of lo
-          const int n = (lo ? 2 : 1) * (D / 64);
-#pragma unroll 1
-          for (int x = 0; x < n; ++x)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(d, q + (x & (D / 64 - 1)) * 32 + 8 * k,
-                     desc_sw128(base + x * Cfg::SUBT + k * 32, 16, 1024), ID_S, x > 0 || k > 0);
-          mma_commit(s_full + 8 * t);
-        }
-        __syncwarp();
-      };
-      auto values = [&](int t, int sg, bool first) {
-        const uint32_t base = uniform(sb + Cfg::V_OFF + sg * Cfg::OPND);
-        const uint32_t d = uniform(tm + 256 * t + 128), p = uniform(tm + 256 * t + 64);
-        const bool acc = uniform(!first);
-        if (elect()) {
-#pragma unroll
-          for (int k = 0; k < TN / 16; ++k)
-            mma_ts(d, p + 8 * k, desc_sw128(base + k * 2048, Cfg::SUBT, 1024), ID_O, acc || k > 0);
-          mma_commit(o_done + 8 * t);
-        }
-        __syncwarp();
-      };
-      auto release = [&](uint32_t bar) {
-        if (elect()) mma_commit(bar);
-        __syncwarp();
-      };
-      auto next_k = [&]() {  // wait for the next K tile; returns its stage
-        ok = ok && warp_wait(k_full + 8 * ks, kph, stop);
-        fence_after();
-        const int sg = ks;
-        if (++ks == KST) {
-          ks = 0;
-          kph ^= 1;
-        }
-        return sg;
-      };
-      auto next_v = [&]() {
-        ok = ok && warp_wait(v_full + 8 * vs, vph, stop);
-        fence_after();
-        const int sg = vs;
-        if (++vs == VST) {
-          vs = 0;
-          vph ^= 1;
-        }
-        return sg;
-      };
-      auto wait_on = [&](uint32_t bar, uint32_t& bits, int t) {
-        ok = ok && warp_wait(bar + 8 * t, (bits >> t) & 1, stop);
-        bits ^= 1u << t;
-        fence_after();
-      };
       while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
-        wait_on(q_full, qph, 0);
-        wait_on(q_full, qph, 1);
-        // Scores x = 0, 1, ... go to stream x mod 2 and their products two steps later: two
-        // row tiles over each token tile, or one over token tiles in turn.
-        const bool two = w.nrt == 2;
-        const int n = (w.e - w.s) * (two ? 2 : 1);
-        int kg = 0, vg = 0;
+        const int n = w.e - w.s;
+        ok = warp_wait(q_full, qph, stop);
+        qph ^= 1;
 #pragma unroll 1
-        for (int x = 0; x < n + 2 && ok; ++x) {
+        for (int x = 0; x < n && ok; ++x) {
           const int t = x & 1;
-          if (x >= 2) {
-            if (!two || t == 0) vg = next_v();
-            wait_on(p_full, pph, t);
-            if (!ok) break;
-            values(t, vg, x < 4);
-            if (!two || t == 1) release(v_empty + 8 * vg);
+          ok = warp_wait(k_full + 8 * sg, kph, stop);
+          if (t == 0) {  // the buffer's last probabilities have been used
+            ok = ok && warp_wait(o_done + 8 * buf, (oph >> buf) & 1, stop);
+            oph ^= 1u << buf;
           }
-          if (x < n) {
-            if (!two || t == 0) kg = next_k();
-            if (!ok) break;
-            scores(t, kg);
-            if (!two || t == 1) release(k_empty + 8 * kg);
+          if (!ok) break;
+          fence_after();
+          const uint32_t base = uniform(sb + sg * Cfg::KSTAGE);
+          const uint32_t d = uniform(tm + 256 + 128 * buf + 64 * t);
+          // sub-tiles of 64 channels: those of hi, then those of lo
+          const int subs = uniform((M.has_lo[sg] ? 2 : 1) * (D / 64));
+          if (elect()) {
+#pragma unroll 1
+            for (int y = 0; y < subs; ++y)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(d, tm + (y & (D / 64 - 1)) * 32 + 8 * k,
+                       desc_sw128(base + y * Cfg::SUBT + k * 32, 16, 1024), ID_S, y > 0 || k > 0);
+            mma_commit(s_full + 16 * buf + 8 * t);
+            mma_commit(k_empty + 8 * sg);
           }
+          __syncwarp();
+          if (++sg == KST) {
+            sg = 0;
+            kph ^= 1;
+          }
+          if (t == 1 || x == n - 1) buf ^= 1;
+        }
+      }
+    } else if (warp == 19) {
+      // ---- products of the probabilities with V ----------------------------------------
+      constexpr uint32_t ID_O = idesc_f16(TM_ROWS, D, true);
+      int sg = 0, buf = 0;
+      uint32_t vph = 0, pph = 0;
+      bool ok = true;
+      while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
+        const int n = w.e - w.s;
+#pragma unroll 1
+        for (int x = 0; x < n && ok; ++x) {
+          const int t = x & 1, i = 2 * buf + t;
+          ok = warp_wait(v_full + 8 * sg, vph, stop) &&
+               warp_wait(p_full + 8 * i, (pph >> i) & 1, stop);
+          pph ^= 1u << i;
+          if (!ok) break;
+          fence_after();
+          const uint32_t base = uniform(sb + Cfg::V_OFF + sg * Cfg::OPND);
+          const uint32_t p = uniform(tm + 256 + 128 * buf + 64 * t);
+          const bool acc = uniform(x > 0), last = uniform(t == 1 || x == n - 1);
+          if (elect()) {
+#pragma unroll
+            for (int k = 0; k < TN / 16; ++k)
+              mma_ts(tm + 64, p + 8 * k, desc_sw128(base + k * 2048, Cfg::SUBT, 1024), ID_O,
+                     acc || k > 0);
+            mma_commit(v_empty + 8 * sg);
+            if (last) mma_commit(o_done + 8 * buf);
+          }
+          __syncwarp();
+          if (++sg == VST) {
+            sg = 0;
+            vph ^= 1;
+          }
+          if (last) buf ^= 1;
         }
       }
     } else if (warp == 18) {
@@ -787,28 +773,29 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     }
   } else if (warp >= 8) {
     // ---- unpacking -------------------------------------------------------------------
-    if (!(warp & 2)) unpack_role<D, ASYM, true>(st, A, smem, M, k_full, k_empty, raw_full, warp, lane);
-    else unpack_role<D, ASYM, false>(st, A, smem, M, v_full, v_empty, raw_full, warp, lane);
+    if (!(warp & 2))
+      unpack_role<D, ASYM, true>(st, A, smem, M, k_full, k_empty, raw_full, warp, lane);
+    else
+      unpack_role<D, ASYM, false>(st, A, smem, M, v_full, v_empty, raw_full, warp, lane);
   } else {
-    // ---- softmax: thread = row ---------------------------------------------------------
+    // ---- softmax: thread = row, group t the token tiles s + t, s + t + 2, ... ----------
     Seg w;
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t base = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tq = base + 256 * t, ts = tq + 64, to = tq + 128;
-    uint32_t sph = 0, oph = 0;
-    int par = 0, tiles_before = 0;  // segment parity; tiles of the segments before
+    const uint32_t to = base + 64 + t * (D / 2);  // this group's half of O's columns
+    uint32_t sph = 0, oph = 0;                    // next phases of the buffers' barriers
+    int buf = 0, par = 0, tiles = 0;  // buffer; segment parity; tiles of the segments before
     bool ok = true;
     constexpr float SLACK = 8.f, BOOST = 7.f, NONE = -1e30f;
     while (next_seg(&M.walk[warp], M, A, st, lane, w)) {
       // This thread's row: node and query head of the group.
-      const bool split = w.nrt == 1;  // streams share the rows and halve the tiles
-      const int r = w.row0 + (split ? row : t * TM_ROWS + row);
+      const int r = w.row0 + row;
       const bool mine = r < rows_of(w.cnt, st.G);
-      const int node = mine ? r / st.G : 0, gh = r - node * st.G;
-      const size_t qrow = (((size_t)w.z * A.m + node) * st.Hq + w.h * st.G + (mine ? gh : 0)) * D;
+      const int node = mine ? r / st.G : 0, gh = mine ? r - node * st.G : 0;
+      const size_t qrow = (((size_t)w.z * A.m + node) * st.Hq + w.h * st.G + gh) * D;
       const bool idle = !__any_sync(0xffffffffu, mine);  // a warp without rows
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = t * (D / 64); c < (t + 1) * (D / 64); ++c) {  // half of Q's columns
         uint32_t x[16];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -816,12 +803,12 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                                : make_uint4(0, 0, 0, 0);
           perm8(v, x + 4 * u);
         }
-        tmem_st16(tq + 16 * c, x);
+        tmem_st16(base + 16 * c, x);
       }
       tmem_wait_st();
       fence_before();
-      // Ancestors of the nodes, one warp: pointer doubling over the parents.
-      if (w.e == w.nt && (warp & 3) == 0 && t == 0) {
+      // Each node's ancestors, by one warp, for the segment that holds the drafts.
+      if (w.e == w.nt && warp == 0) {
         for (int i = lane; i < 64; i += 32) {
           unsigned long long a = 0;
           if (i < w.cnt) {
@@ -836,28 +823,34 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         }
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(q_full + 8 * t);
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // both streams: anc is there
+      if (lane == 0) bar_arrive(q_full);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // anc is there
 
       float mref = NONE;
       uint64_t l2 = pack2(0.f, 0.f), z2 = pack2(0.f, 0.f);
-      int done = 0;
-      for (int i = split ? w.s + t : w.s; i < w.e; i += split ? 2 : 1) {
-        // V stages (and the scales with them) go round over all of the CTA's tiles.
-        const int at = tiles_before + (i - w.s), sg = at % VST;
-        ok = ok && warp_wait(sc_full + 8 * sg, (at / VST) & 1, stop);
-        ok = ok && warp_wait(s_full + 8 * t, sph, stop);
-        if (!ok) break;
-        sph ^= 1;
-        fence_after();
-        if (!idle) {
-          const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
-          const unsigned long long seen =
-              *reinterpret_cast<const unsigned long long*>(M.valid[sg]) &
-              (i == w.nt - 1 ? M.anc[par][node] : ~0ull);
-          const bool part = __any_sync(0xffffffffu, seen != ~0ull);
-          // Scores are read from tensor memory twice, 32 columns at a time (short loops
-          // keep the roles' code within the instruction caches).
+      const int n = w.e - w.s;
+#pragma unroll 1
+      for (int x0 = 0; x0 < n; x0 += 2) {
+        const bool have = x0 + t < n && !idle;
+        const int at = tiles + x0 + t, sg = at % VST;  // V stages go round over all tiles
+        const uint32_t ts = base + 256 + 128 * buf + 64 * t;
+        const int bi = 2 * buf + t;
+        if (x0 + t < n) {
+          ok = ok && warp_wait(sc_full + 8 * sg, (at / VST) & 1, stop);
+          ok = ok && warp_wait(s_full + 8 * bi, (sph >> bi) & 1, stop);
+          sph ^= 1u << bi;
+          fence_after();
+        }
+        const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
+        unsigned long long seen = ~0ull;
+        bool part = false;
+        float mnew = -CUDART_INF_F;
+        // Scores are read from tensor memory twice, 32 columns at a time (short loops
+        // keep the roles' code within the instruction caches).
+        if (have && ok) {
+          seen = *reinterpret_cast<const unsigned long long*>(M.valid[sg]) &
+                 (w.s + x0 + t == w.nt - 1 ? M.anc[par][node] : ~0ull);
+          part = __any_sync(0xffffffffu, seen != ~0ull);
           float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
@@ -869,7 +862,8 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             for (int c = 0; c < 8; ++c) {  // x + log2 s
               const ulonglong2 a = lv[c];
               unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), sl2, a.x), x[4 * c], x[4 * c + 1]);
-              unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), sl2, a.y), x[4 * c + 2], x[4 * c + 3]);
+              unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), sl2, a.y), x[4 * c + 2],
+                      x[4 * c + 3]);
             }
             if (part) {
               const uint32_t bits = (uint32_t)(seen >> (32 * hf));
@@ -881,19 +875,31 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             for (int c = 0; c < 32; c += 2)
               mx[c >> 1 & 3] = fmaxf(mx[c >> 1 & 3], fmaxf(x[c], x[c + 1]));
           }
-          const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
+        int moves;
+        asm volatile(
+            "{ .reg .pred p, q; setp.ne.s32 p, %1, 0; "
+            "barrier.cta.red.or.pred.aligned q, 2, 256, p; selp.s32 %0, 1, 0, q; }"
+            : "=r"(moves)
+            : "r"((int)(mnew > mref + SLACK))
+            : "memory");
+        if (moves) {  // some row's reference moves
+          M.mx[t][row] = mnew;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          mnew = fmaxf(mnew, M.mx[t ^ 1][row]);
           const bool move = mnew > mref + SLACK;
-          if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? ex2(mref - mnew) : 1.f;
-            if (move) mref = mnew;
-            if (done > 0) {  // O holds this stream's products up to the tile before
-              ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
-              if (!ok) break;
-              fence_after();
-              l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
-              if (ASYM) z2 = fma2(z2, pack2(f, f), pack2(0.f, 0.f));
+          const float f = move ? ex2(mref - mnew) : 1.f;
+          if (move) mref = mnew;
+          l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
+          if (ASYM) z2 = fma2(z2, pack2(f, f), pack2(0.f, 0.f));
+          if (x0 > 0 && ok) {  // O holds the products up to the pair before: rescale it
+            const int ob = buf ^ 1;
+            ok = warp_wait(o_done + 8 * ob, (oph >> ob & 1) ^ 1, stop);
+            fence_after();
+            if (ok && !idle) {
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
+              for (int c = 0; c < D / 2; c += 16) {
                 uint32_t v[16];
                 tmem_ld16(to + c, v);
                 tmem_wait_ld();
@@ -901,8 +907,14 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                 for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) * f);
                 tmem_st16(to + c, v);
               }
+              tmem_wait_st();
             }
           }
+          fence_before();
+          asm volatile("bar.sync 1, 256;" ::: "memory");  // before any product of this pair
+          fence_after();
+        }
+        if (have && ok) {
           const uint64_t off = pack2(BOOST - mref, BOOST - mref);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
@@ -944,61 +956,44 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
           tmem_wait_st();
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(p_full + 8 * t);
-        oph ^= 1;
-        ++done;
+        if (x0 + t < n) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(p_full + 8 * bi);
+        }
+        oph ^= 1u << buf;
+        buf ^= 1;
       }
-      if (ok && done) ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
+      const int ob = buf ^ 1;  // the last pair's products
+      ok = ok && warp_wait(o_done + 8 * ob, (oph >> ob & 1) ^ 1, stop);
       fence_after();
-      float la, lb, za, zb;
-      unpack2(l2, la, lb);
-      unpack2(z2, za, zb);
-      float l = la + lb, zs = za + zb, m = mref, f0 = 1.f, f1 = 0.f;
-      int c0 = 0, c1 = D;  // the columns this thread writes
-      float z0 = zs, z1 = 0.f;
-      if (split) {  // the other stream's share of the row; each writes half the columns
-        M.ml[t][0][row] = m;
-        M.ml[t][1][row] = l;
-        M.ml[t][2][row] = zs;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const float m0 = M.ml[0][0][row], m1 = M.ml[1][0][row];
-        const float l0 = M.ml[0][1][row], l1 = M.ml[1][1][row];
-        m = fmaxf(m0, m1);
-        f0 = ex2(m0 - m);
-        f1 = ex2(m1 - m);
-        l = f0 * l0 + f1 * l1;
-        z0 = M.ml[0][2][row];
-        z1 = M.ml[1][2][row];
-        c0 = t * (D / 2);
-        c1 = c0 + D / 2;
+      {
+        float la, lb, za, zb;
+        unpack2(l2, la, lb);
+        unpack2(z2, za, zb);
+        M.lz[t][0][row] = la + lb;
+        M.lz[t][1][row] = za + zb;
       }
-      const bool second = split && w.e - w.s > 1;  // the other stream had a tile
-      const uint32_t oa = split ? base + 128 : to, ob = base + 256 + 128;
-      const float add = f0 * z0 + f1 * z1;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float l = M.lz[0][0][row] + M.lz[1][0][row], add = M.lz[0][1][row] + M.lz[1][1][row];
       const bool direct = w.whole();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int rt = split ? 0 : t;
-      float4* part = reinterpret_cast<float4*>(A.acc) +
-                     ((size_t)w.slot * 2 + rt) * (D / 4) * TM_ROWS;
-      if (!direct && mine && c0 == 0)
-        A.ml[((size_t)w.slot * 2 + rt) * TM_ROWS + row] = make_float2(m, l);
+      float4* part4 = reinterpret_cast<float4*>(A.acc) + (size_t)w.slot * (D / 4) * TM_ROWS;
+      if (!direct && mine && t == 0) A.ml[(size_t)w.slot * TM_ROWS + row] = make_float2(mref, l);
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 16) {
-        uint32_t x[16], x1[16];
-        tmem_ld16(oa + c, x);
-        if (second) tmem_ld16(ob + c, x1);
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t x[16];
+        tmem_ld16(to + c, x);
         tmem_wait_ld();
+        if (!mine) continue;
         float v[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
           // natural channel u of the 16: position in the unpacked order
           const int at = (u & 8) + ((u & 4) ? 2 * (u & 3) + 1 : 2 * (u & 3));
-          v[u] = f0 * __uint_as_float(x[at]) + add;
-          if (second) v[u] = fmaf(f1, __uint_as_float(x1[at]), v[u]);
+          v[u] = __uint_as_float(x[at]) + add;
         }
-        if (!mine) continue;
+        const int ch = t * (D / 2) + c;
         if (direct) {
           uint32_t hw[8];
 #pragma unroll
@@ -1007,19 +1002,19 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                                        : __floats2half2_rn(0.f, 0.f);
             hw[u] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          uint4* dst = reinterpret_cast<uint4*>(A.o + qrow + c);
+          uint4* dst = reinterpret_cast<uint4*>(A.o + qrow + ch);
           dst[0] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
           dst[1] = make_uint4(hw[4], hw[5], hw[6], hw[7]);
         } else {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            part[(size_t)(c / 4 + u) * TM_ROWS + row] =
+            part4[(size_t)(ch / 4 + u) * TM_ROWS + row] =
                 make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
         }
       }
       fence_before();
-      if (split) asm volatile("bar.sync 1, 256;" ::: "memory");  // both accumulators are read
-      tiles_before += w.e - w.s;
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the accumulator and lz are read
+      tiles += n;
       par ^= 1;
     }
     if (!ok && lane == 0) set_error(st, EKV_ETIMEOUT);
@@ -1049,10 +1044,10 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
   const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
   const int rows = rows_of(cnt, st.G);
   if (rt * TM_ROWS >= rows) return;
-  const int nt = tiles_of(len), cost = tile_cost(rows);
+  const int nt = tiles_of(len);
   const int64_t total = A.pre[A.n_seqs];
-  const int64_t a = A.pre[z] + (int64_t)(h * pairs_of(rows) + rt / 2) * nt * cost;
-  const int64_t b = a + (int64_t)nt * cost;
+  const int64_t a = A.pre[z] + (int64_t)(h * row_tiles(rows) + rt) * nt;
+  const int64_t b = a + nt;
   int c0 = (int)(a * A.grid / total);  // the run that holds a
   while (c0 > 0 && run_start(total, c0, A.grid) > a) --c0;
   while (run_start(total, c0 + 1, A.grid) <= a) ++c0;
@@ -1062,7 +1057,7 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
   for (int i = row; i < n; i += TM_ROWS) {
     int s, e;
     const int64_t lo = run_start(total, c0 + i, A.grid);
-    unit_part(a, nt, cost, lo, run_start(total, c0 + i + 1, A.grid), s, e);
+    unit_part(a, nt, lo, run_start(total, c0 + i + 1, A.grid), s, e);
     s_slot[i] = s == 0 && e == nt ? -2 : s < e ? 2 * (c0 + i) + (lo > a ? 0 : 1) : -1;
   }
   __syncthreads();
@@ -1071,7 +1066,7 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
   float m = -1e30f;
   for (int i = 0; i < n; ++i) {
     if (s_slot[i] == -2) return;
-    if (s_slot[i] >= 0) m = fmaxf(m, A.ml[((size_t)s_slot[i] * 2 + (rt & 1)) * TM_ROWS + row].x);
+    if (s_slot[i] >= 0) m = fmaxf(m, A.ml[(size_t)s_slot[i] * TM_ROWS + row].x);
   }
   const int node = r / st.G, gh = r - node * st.G;
   __half* dst = A.o + (((size_t)z * A.m + node) * st.Hq + h * st.G + gh) * D;
@@ -1081,7 +1076,7 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       if (s_slot[i] < 0) continue;
-      const size_t at = (size_t)s_slot[i] * 2 + (rt & 1);
+      const size_t at = (size_t)s_slot[i];
       const float2 ml = A.ml[at * TM_ROWS + row];
       const float4 x = reinterpret_cast<const float4*>(A.acc)[(at * (D / 4) + g) * TM_ROWS + row];
       const float f = ex2(ml.x - m);
@@ -1143,7 +1138,7 @@ struct TreeScratch {
   int grid = 0;
   size_t acc = 0, ml = 0, pre = 0, bytes = 0;
 };
-// One CTA an SM; two partials a CTA (its first and its last segment) of two row tiles.
+// One CTA an SM; two partials a CTA (its first and its last segment).
 int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1152,7 +1147,7 @@ int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
     return EKV_ECUDA;
   }
   if (t->grid > 256) t->grid = 256;  // the merging kernel's table of parts
-  const size_t parts = (size_t)t->grid * 2 * 2 * TM_ROWS;
+  const size_t parts = (size_t)t->grid * 2 * TM_ROWS;
   const int n = n_seqs < TSEQS ? n_seqs : TSEQS;
   t->acc = 0;
   t->ml = parts * st.D * sizeof(float);
