@@ -11,14 +11,14 @@
 // (1 to 512), so each page is worth 16 keys to all of them: it is read from memory and
 // unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
 // tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
-//   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
-//   warps 8-15   unpack the K (8, 9, 12, 13) and the V parts of a raw tile, a page a warp
-//                (K and V on different schedulers: less code for each), into swizzled
-//                fp16 operand tiles: K as hi + lo (khat = code * scale = hi + lo exactly,
-//                two products; 2- and 16-bit K need hi alone), V as the bare codes (exact
-//                in fp16)
-//   warp 18      the V scales of a tile, for softmax
-//   warps 16, 19 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
+//   warp 25      page copies (cp.async.bulk) into a ring of raw tiles
+//   warps 8-23   two sets that take the tiles in turn: unpack the K (8, 9, 12, 13) and the
+//                V parts of a raw tile, a page a warp (K and V on different schedulers: less
+//                code for each), into swizzled fp16 operand tiles: K as hi + lo
+//                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K need
+//                hi alone), V as the bare codes (exact in fp16)
+//   warp 26      the V scales of a tile, for softmax
+//   warps 24, 27 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
 //                their waits in one loop took longer than the products)
 //   warps 0-3, 4-7  softmax, one row a thread; the two groups take the even and the odd
 //                token tiles of a pair, for the same rows
@@ -51,8 +51,11 @@ using namespace tc;
 constexpr int TM_ROWS = 128;      // rows of a row tile
 constexpr int TN = 64;            // tokens of a token tile
 constexpr int TPAGES = TN / BLOCK;
-constexpr int TT = 640;           // threads
-constexpr int TSEQS = 512;        // sequences of one launch
+constexpr int TT = 896;           // threads
+constexpr int SETS = 2;           // sets of unpacking warps, taking the tiles in turn
+constexpr int W_SCORES = 8 + 8 * SETS, W_PAGES = W_SCORES + 1, W_SCALES = W_SCORES + 2,
+              W_VALUES = W_SCORES + 3;
+constexpr int TSEQS = 256;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
 constexpr int VST = 4;            // V operand tiles in flight (until their products are done)
 constexpr int RAW_BYTES = 80 * 1024;
@@ -67,6 +70,24 @@ struct TCfg {
   static constexpr int RAW_OFF = V_OFF + VST * OPND;
   static constexpr int MISC_OFF = RAW_OFF + RAW_BYTES;
 };
+
+// Runs of equal length: run c starts at total * c / grid = quot * c + rest * c / grid.
+struct Runs {
+  int64_t quot;
+  int rest, grid;
+  __device__ void init(int64_t total, int g) {
+    grid = g;
+    quot = total / g;
+    rest = (int)(total - quot * g);
+  }
+  __device__ int64_t start(int c) const { return quot * c + rest * c / grid; }
+};
+// Raw tiles in flight for pages of `room` bytes: an even number, so that each ring slot is
+// always the same unpacking set's (a set that skipped a slot's use could take the phase
+// before for its own).  The drafts' tile takes a slot too, without copies.
+__device__ __forceinline__ int raw_tiles(int room) {
+  return min(RAW_MAX, RAW_BYTES / (TPAGES * room)) / SETS * SETS;
+}
 
 // A segment: the token tiles s .. e-1 of one unit.
 struct TMisc;
@@ -103,6 +124,7 @@ struct TMisc {
   float mx[2][TM_ROWS];         // row maxima of the two groups, then their (sum, z)
   float lz[2][2][TM_ROWS];
   alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 1 + 4 + 4 + 2];
+  Runs runs;
   Walk walk[TT / 32];
   int stop;
   uint32_t tmem;
@@ -126,9 +148,6 @@ __host__ __device__ inline int64_t seq_tiles(int len, int cnt, int G, int Hkv) {
   const int r = rows_of(cnt, G);
   return cnt > 0 ? (int64_t)Hkv * row_tiles(r) * tiles_of(len) : 0;
 }
-__host__ __device__ inline int64_t run_start(int64_t total, int c, int grid) {
-  return total * c / grid;
-}
 // Tiles of a unit of nt tiles at offset a that lie in the run [lo, hi).
 __host__ __device__ inline void unit_part(int64_t a, int nt, int64_t lo, int64_t hi, int& s,
                                           int& e) {
@@ -143,10 +162,9 @@ __device__ __forceinline__ int Seg::tokens(int i, const TMisc& M, int rs, int pg
 }
 
 // First step: the sequence that holds the run's start.
-__device__ __noinline__ void walk_init(Walk* w, const TMisc& M, int n_seqs, int grid) {
-  const int64_t total = M.pre[n_seqs];
-  w->lo = run_start(total, blockIdx.x, grid);
-  w->hi = run_start(total, blockIdx.x + 1, grid);
+__device__ __noinline__ void walk_init(Walk* w, const TMisc& M, int n_seqs) {
+  w->lo = M.runs.start(blockIdx.x);
+  w->hi = M.runs.start(blockIdx.x + 1);
   int p = 0, q = n_seqs;  // the last sequence that starts at or before the run
   while (q - p > 1) {
     const int mid = (p + q) / 2;
@@ -170,7 +188,8 @@ __device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int 
       w->a = M.pre[z];
       w->unit = 0;
       if (w->nunits && w->lo > w->a) {  // skip the units before the run
-        const int64_t skip = (w->lo - w->a) / w->nt;
+        const int64_t d = w->lo - w->a;
+        const int64_t skip = d >> 31 ? d / w->nt : (uint32_t)d / (uint32_t)w->nt;
         w->unit = (int)(skip < w->nunits ? skip : w->nunits);
         w->a += (int64_t)w->unit * w->nt;
       }
@@ -425,30 +444,44 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
   Seg w;
   const int kmax = max(2, st.kmax[A.layer]);
   const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
-  const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
+  const int nraw = raw_tiles(page_room);
   const int pg = (warp & 1) + (warp >> 1 & 2);  // page of the tile
   const Lane<D> hf(lane);
-  int rs = 0, sg = 0;
+  const int set = (warp >> 3) - 1;
+  int rs = 0, sg = 0, turn = 0;
   uint32_t rph = 0, eph = 1;
   bool ok = true;
   while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
     for (int i = w.s; i < w.e; ++i) {
       const bool drafts = i == w.nt - 1;
-      ok = ok && warp_wait(out_empty + 8 * sg, eph, stop);
-      if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+      const int at = sg, raw = rs;
+      const uint32_t full_phase = rph, empty_phase = eph;
+      if (++sg == (IS_K ? KST : VST)) {
+        sg = 0;
+        eph ^= 1;
+      }
+      if (++rs == nraw) {
+        rs = 0;
+        rph ^= 1;
+      }
+      const bool other = turn != set;  // another set's tile
+      if (++turn == SETS) turn = 0;
+      if (other) continue;
+      ok = ok && warp_wait(out_empty + 8 * at, empty_phase, stop);
+      ok = ok && warp_wait(raw_full + 8 * raw, full_phase, stop);
       if (!ok) break;
       uint8_t* dst = smem + pg * BLOCK * 128 +
-                     (IS_K ? sg * Cfg::KSTAGE : Cfg::V_OFF + sg * Cfg::OPND);
+                     (IS_K ? at * Cfg::KSTAGE : Cfg::V_OFF + at * Cfg::OPND);
       // Where the part's rows are and how many hold tokens: in the raw tile; the open
       // block's K in the staging rows and V in its page, in memory; the drafts as given.
-      const int n = w.tokens(i, M, rs, pg);
-      const int32_t e = drafts ? -1 : M.ent[rs][pg];
+      const int n = w.tokens(i, M, raw, pg);
+      const int32_t e = drafts ? -1 : M.ent[raw][pg];
       const int kb = bits_of_code(entry_fmt(e) >> 2);
       if constexpr (IS_K) {
-        const bool lo = !drafts && M.raw_lo[rs] != 0;
-        if (pg == 0 && lane == 0) M.has_lo[sg] = lo;
+        const bool lo = !drafts && M.raw_lo[raw] != 0;
+        if (pg == 0 && lane == 0) M.has_lo[at] = lo;
         if (n == BLOCK && !drafts) {
-          const uint8_t* page = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room;
+          const uint8_t* page = smem + Cfg::RAW_OFF + (raw * TPAGES + pg) * page_room;
           switch (kb) {
             case 2: unpack_k<D, 2, ASYM, true>(page, D / 4, n, dst, lo, hf); break;
             case 4: unpack_k<D, 4, ASYM, true>(page, D / 2, n, dst, lo, hf); break;
@@ -464,7 +497,7 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
         }
       } else {
         const int fmt = entry_fmt(e), v_off = k_part_bytes(kb, D, ASYM);
-        const uint8_t* vp = smem + Cfg::RAW_OFF + (rs * TPAGES + pg) * page_room + v_off;
+        const uint8_t* vp = smem + Cfg::RAW_OFF + (raw * TPAGES + pg) * page_room + v_off;
         int64_t stride = D * A.vb / 8;
         int vb = A.vb;
         if (drafts) {
@@ -485,16 +518,8 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        bar_arrive(out_full + 8 * sg);
-        if (!drafts) bar_arrive(raw_empty + 8 * rs);
-      }
-      if (++sg == (IS_K ? KST : VST)) {
-        sg = 0;
-        eph ^= 1;
-      }
-      if (!drafts && ++rs == nraw) {
-        rs = 0;
-        rph ^= 1;
+        bar_arrive(out_full + 8 * at);
+        bar_arrive(raw_empty + 8 * raw);
       }
     }
   }
@@ -548,7 +573,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     M.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tmem_alloc(smem_u32(&M.tmem), 512);
+  if (warp == W_SCORES) tmem_alloc(smem_u32(&M.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
@@ -568,22 +593,25 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       if (z < A.n_seqs) M.pre[z] = run + x - c;
       run += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) M.pre[A.n_seqs] = run;
+    if (lane == 0) {
+      M.pre[A.n_seqs] = run;
+      M.runs.init(run, A.grid);
+    }
     __syncwarp();
     if (blockIdx.x == 0)
       for (int z = lane; z <= A.n_seqs; z += 32) A.pre[z] = M.pre[z];
   }
   __syncthreads();
-  if (lane == 0) walk_init(&M.walk[warp], M, A.n_seqs, A.grid);
+  if (lane == 0) walk_init(&M.walk[warp], M, A.n_seqs);
   __syncwarp();
 
-  if (warp >= 16) {
+  if (warp >= W_SCORES) {
     Seg w;
     // Raw tile: 4 pages, each sized for the widest page the layer has admitted.
     const int kmax = max(2, st.kmax[A.layer]);
     const int page_room = (page_bytes(kmax, A.vb, D, ASYM) + 127) & ~127;
-    const int nraw = min(RAW_MAX, RAW_BYTES / (TPAGES * page_room));
-    if (warp == 17) {
+    const int nraw = raw_tiles(page_room);
+    if (warp == W_PAGES) {
       // ---- page copies ---------------------------------------------------------------
       int rs = 0;
       uint32_t ph = 1;
@@ -591,9 +619,9 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
         const int32_t* bt = st.bt + lsh_index(st, A.layer, M.slot[w.z], w.h) * st.maxblk;
         const int nblk = (w.len + BLOCK - 1) / BLOCK, sealed = w.len / BLOCK;
-        const int end = min(w.e, w.nt - 1);  // the drafts' tile has no pages
+        // (the drafts' tile, the last, has no pages: its blocks lie behind the table's use)
         int32_t ahead = -1;
-        for (int i = w.s; i < end && ok; ++i) {
+        for (int i = w.s; i < w.e && ok; ++i) {
           const int k = (i - w.s) & 7;
           if (k == 0) {  // table entries of the next 8 tiles
             const int b = i * TPAGES + lane;
@@ -634,7 +662,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
         }
       }
-    } else if (warp == 16) {
+    } else if (warp == W_SCORES) {
       // ---- scores of token tile x into buffer (x / 2) mod 2 of group x mod 2 -----------
       constexpr uint32_t ID_S = idesc_f16(TM_ROWS, TN, false);
       int sg = 0, buf = 0;
@@ -676,7 +704,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           if (t == 1 || x == n - 1) buf ^= 1;
         }
       }
-    } else if (warp == 19) {
+    } else if (warp == W_VALUES) {
       // ---- products of the probabilities with V ----------------------------------------
       constexpr uint32_t ID_O = idesc_f16(TM_ROWS, D, true);
       int sg = 0, buf = 0;
@@ -711,7 +739,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           if (last) buf ^= 1;
         }
       }
-    } else if (warp == 18) {
+    } else if (warp == W_SCALES) {
       // ---- V scales and which tokens there are, two tokens a lane -------------------
       int rs = 0, vs = 0;
       uint32_t rph = 0, eph = 1;
@@ -720,7 +748,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         for (int i = w.s; i < w.e; ++i) {
           const bool drafts = i == w.nt - 1;
           ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
-          if (!drafts) ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+          ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
           if (!ok) break;
           int n = drafts ? min(TN, w.cnt) : min(TN, w.len - i * TN);  // tokens of the tile
 #pragma unroll
@@ -758,13 +786,13 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           __syncwarp();
           if (lane == 0) {
             bar_arrive(sc_full + 8 * vs);
-            if (!drafts) bar_arrive(raw_empty + 8 * rs);
+            bar_arrive(raw_empty + 8 * rs);
           }
           if (++vs == VST) {
             vs = 0;
             eph ^= 1;
           }
-          if (!drafts && ++rs == nraw) {
+          if (++rs == nraw) {
             rs = 0;
             rph ^= 1;
           }
@@ -1020,7 +1048,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     if (!ok && lane == 0) set_error(st, EKV_ETIMEOUT);
   }
   __syncthreads();
-  if (warp == 16) {
+  if (warp == W_SCORES) {
     fence_after();
     if (*stop) {
       if (lane == 0) set_error(st, EKV_ETIMEOUT);
@@ -1031,11 +1059,13 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
 }
 
 // Merge the partials of the units that run ends cut: a thread per (row, 4 channels).
+constexpr int MAX_GRID = 256;
 template <int D>
 __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeArgs A, int rt_max,
                                                              int groups) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int s_slot[256];
+  __shared__ int64_t s_start[MAX_GRID + 1];
+  __shared__ int s_slot[MAX_GRID];
+  __shared__ Runs s_runs;
   const int rt = blockIdx.x % rt_max, h = blockIdx.x / rt_max % st.Hkv;
   const int z = blockIdx.x / rt_max / st.Hkv, row = threadIdx.x;
   const int slot = A.slots[z];
@@ -1044,47 +1074,68 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
   const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
   const int rows = rows_of(cnt, st.G);
   if (rt * TM_ROWS >= rows) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row == 0) s_runs.init(A.pre[A.n_seqs], A.grid);
+  __syncthreads();
+  for (int i = row; i <= A.grid; i += TM_ROWS) s_start[i] = s_runs.start(i);
+  __syncthreads();
+  // The runs that hold parts of this unit, [a, a + nt): c0 .. c1 - 1.
   const int nt = tiles_of(len);
-  const int64_t total = A.pre[A.n_seqs];
   const int64_t a = A.pre[z] + (int64_t)(h * row_tiles(rows) + rt) * nt;
-  const int64_t b = a + nt;
-  int c0 = (int)(a * A.grid / total);  // the run that holds a
-  while (c0 > 0 && run_start(total, c0, A.grid) > a) --c0;
-  while (run_start(total, c0 + 1, A.grid) <= a) ++c0;
-  int n = 1;
-  while (c0 + n < A.grid && run_start(total, c0 + n, A.grid) < b) ++n;
-  if (n == 1) return;  // one CTA had the whole unit and wrote o
-  for (int i = row; i < n; i += TM_ROWS) {
-    int s, e;
-    const int64_t lo = run_start(total, c0 + i, A.grid);
-    unit_part(a, nt, lo, run_start(total, c0 + i + 1, A.grid), s, e);
-    s_slot[i] = s == 0 && e == nt ? -2 : s < e ? 2 * (c0 + i) + (lo > a ? 0 : 1) : -1;
+  int c0 = 0, c1 = 0;
+  for (int i0 = 0; i0 < A.grid; i0 += TM_ROWS) {
+    const int i = i0 + row;
+    c0 += __syncthreads_count(i < A.grid && s_start[i + 1] <= a);
+    c1 += __syncthreads_count(i < A.grid && s_start[i] < a + nt);
+  }
+  if (c1 - c0 == 1) return;  // one CTA had the whole unit and wrote o
+  for (int i = row; c0 + i < c1; i += TM_ROWS) {
+    const int c = c0 + i;
+    s_slot[i] = s_start[c] == s_start[c + 1] ? -1 : 2 * c + (s_start[c] > a ? 0 : 1);
   }
   __syncthreads();
-  const int r = rt * TM_ROWS + row;
+  const int r = rt * TM_ROWS + row, n = c1 - c0;
   if (r >= rows) return;
+  constexpr int U = 8;  // partials in flight
   float m = -1e30f;
-  for (int i = 0; i < n; ++i) {
-    if (s_slot[i] == -2) return;
-    if (s_slot[i] >= 0) m = fmaxf(m, A.ml[(size_t)s_slot[i] * TM_ROWS + row].x);
+  for (int i = 0; i < n; i += U) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = i + u < n ? s_slot[i + u] : -1;
+      x[u] = k >= 0 ? __ldcg(&A.ml[(size_t)k * TM_ROWS + row].x) : -1e30f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, x[u]);
   }
   const int node = r / st.G, gh = r - node * st.G;
   __half* dst = A.o + (((size_t)z * A.m + node) * st.Hq + h * st.G + gh) * D;
   for (int g = blockIdx.y * groups; g < (int)(blockIdx.y + 1) * groups; ++g) {
     float l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      if (s_slot[i] < 0) continue;
-      const size_t at = (size_t)s_slot[i];
-      const float2 ml = A.ml[at * TM_ROWS + row];
-      const float4 x = reinterpret_cast<const float4*>(A.acc)[(at * (D / 4) + g) * TM_ROWS + row];
-      const float f = ex2(ml.x - m);
-      l = fmaf(f, ml.y, l);
-      v.x = fmaf(f, x.x, v.x);
-      v.y = fmaf(f, x.y, v.y);
-      v.z = fmaf(f, x.z, v.z);
-      v.w = fmaf(f, x.w, v.w);
+    for (int i = 0; i < n; i += U) {
+      float2 ml[U];
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u < n ? s_slot[i + u] : -1;
+        ml[u] = make_float2(-1e30f, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= 0) {
+          ml[u] = __ldcg(&A.ml[(size_t)k * TM_ROWS + row]);
+          x[u] = __ldcg(reinterpret_cast<const float4*>(A.acc) +
+                        ((size_t)k * (D / 4) + g) * TM_ROWS + row);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = ml[u].y > 0.f ? ex2(ml[u].x - m) : 0.f;
+        l = fmaf(f, ml[u].y, l);
+        v.x = fmaf(f, x[u].x, v.x);
+        v.y = fmaf(f, x[u].y, v.y);
+        v.z = fmaf(f, x[u].z, v.z);
+        v.w = fmaf(f, x[u].w, v.w);
+      }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     __align__(8) __half2 hh[2] = {__floats2half2_rn(v.x * inv, v.y * inv),
@@ -1146,7 +1197,7 @@ int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
     cudaGetLastError();
     return EKV_ECUDA;
   }
-  if (t->grid > 256) t->grid = 256;  // the merging kernel's table of parts
+  if (t->grid > MAX_GRID) t->grid = MAX_GRID;  // the merging kernel's table of parts
   const size_t parts = (size_t)t->grid * 2 * TM_ROWS;
   const int n = n_seqs < TSEQS ? n_seqs : TSEQS;
   t->acc = 0;
