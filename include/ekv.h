@@ -511,7 +511,8 @@ EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_
  *   k, v       dev fp16 [n_seqs][max_nodes][Hkv][d]; all four 16-byte aligned
  * o_ih = softmax-weighted sum over every cached token of the sequence (the
  * dequantized page values, as ekv_decode_attn) and over the k, v of node i and
- * its ancestors.  A sequence may have no cached tokens.
+ * its ancestors.  A sequence may have no cached tokens.  The handle's softmax scale
+ * times log2(e) lies in [2^-25, 2^15), else EKV_EUNSUPPORTED.
  *   scratch    dev, 16-byte aligned, ekv_tree_attn_scratch_bytes bytes
  *              (caller-owned; overwritten; one call at a time)
  * Device errors as ekv_decode_attn. */

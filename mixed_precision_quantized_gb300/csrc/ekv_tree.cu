@@ -30,7 +30,10 @@
 //
 // A token's V scale s multiplies its probability: P' = 2^(x + log2 s - m) in fp16, where
 // the reference m follows the largest x + log2 s, so the fp16 range is used well whatever
-// the scales; the row sum adds P' / s in fp32.  As in prompt attention m moves only for
+// the scales; the row sum adds P' / s in fp32.  The log2 s come with the scores: 16 more
+// channels of K hold log2 s / (sigma log2 e) as three fp16 parts, against a constant in Q
+// (each softmax thread loading 64 of them twice from shared memory took longer than the
+// exponentials).  As in prompt attention m moves only for
 // a gain above 2^8, P' carries 2^7, and P' is the one value rounded to fp16.
 //
 // Work split: the token tiles of all (sequence, KV head, row tile) units laid end to end,
@@ -58,14 +61,14 @@ constexpr int W_SCORES = 8 + 8 * SETS, W_PAGES = W_SCORES + 1, W_SCALES = W_SCOR
 constexpr int TSEQS = 256;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
 constexpr int VST = 4;            // V operand tiles in flight (until their products are done)
-constexpr int RAW_BYTES = 80 * 1024;
+constexpr int RAW_BYTES = 64 * 1024;
 constexpr int RAW_MAX = 8;        // raw tiles in flight at most
 
 template <int D>
 struct TCfg {
   static constexpr int SUBT = TN * 128;              // 64 channels of a tile
   static constexpr int OPND = D / 64 * SUBT;         // one operand tile
-  static constexpr int KSTAGE = 2 * OPND;            // hi, lo
+  static constexpr int KSTAGE = 2 * OPND + SUBT;     // hi, lo, 16 more channels
   static constexpr int V_OFF = KST * KSTAGE;
   static constexpr int RAW_OFF = V_OFF + VST * OPND;
   static constexpr int MISC_OFF = RAW_OFF + RAW_BYTES;
@@ -113,8 +116,7 @@ struct TMisc {
   int32_t slot[TSEQS];
   uint8_t cnt[TSEQS];           // nodes
   unsigned long long anc[2][64];  // ancestors-or-self of each node, by segment parity
-  // of each token's V scale s: log2 s, 1 / s and (asymmetric) the zero point over s
-  alignas(16) float lsv[VST][TN];
+  // of each token's V scale s: 1 / s and (asymmetric) the zero point over s
   alignas(16) float rsv[VST][TN];
   alignas(16) float zsv[VST][TN];
   alignas(8) uint16_t valid[VST][TPAGES];  // tokens that are there
@@ -139,6 +141,7 @@ struct TreeArgs {
   float2* ml;       // [2 grid][128] (max, sum)
   int64_t* pre;     // [n_seqs + 1] for the merging kernel
   int grid;
+  float q_ext, k_ext;  // Q's constant c for the log2 s channels, and 1 / (sl c)
 };
 
 __host__ __device__ inline int rows_of(int cnt, int G) { return cnt * G; }
@@ -408,7 +411,7 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
 // V rows at vp into dst; rows from n on become zero.  Codes are signed for both
 // quantizers: u s + z = (u - 2^(b-1)) s + (z + 2^(b-1) s), so that the products P' q stay
 // as small as the values.
-template <int D, int VB>
+template <int D, int VB, bool FULL>
 __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int n, uint8_t* dst,
                                          const Lane<D>& ln) {
   constexpr int STEP = Lane<D>::STEP;
@@ -422,11 +425,12 @@ __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int 
       Raw8<VB> raw[R];
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (c + ln.t0 + (j + i) * STEP < n) raw[i].load(row + (j + i) * STEP * stride, ln.g);
+        if (FULL || c + ln.t0 + (j + i) * STEP < n)
+          raw[i].load(row + (j + i) * STEP * stride, ln.g);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         uint32_t w[4] = {0, 0, 0, 0};
-        if (c + ln.t0 + (j + i) * STEP < n) unpack8w<VB, false>(raw[i], w);
+        if (FULL || c + ln.t0 + (j + i) * STEP < n) unpack8w<VB, false>(raw[i], w);
         *reinterpret_cast<uint4*>(out + ln.off[j + i]) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
@@ -497,22 +501,28 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
         }
       } else {
         const int fmt = entry_fmt(e), v_off = k_part_bytes(kb, D, ASYM);
-        const uint8_t* vp = smem + Cfg::RAW_OFF + (raw * TPAGES + pg) * page_room + v_off;
-        int64_t stride = D * A.vb / 8;
-        int vb = A.vb;
-        if (drafts) {
-          vp = reinterpret_cast<const uint8_t*>(
-              A.v + (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D);
-          stride = 2 * D * (int64_t)st.Hkv;
-          vb = 16;
-        } else if (n > 0 && n < BLOCK) {
-          vp = st.pool_base[fmt] + v_off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt];
-        }
-        switch (vb) {
-          case 2: unpack_v<D, 2>(vp, stride, n, dst, hf); break;
-          case 4: unpack_v<D, 4>(vp, stride, n, dst, hf); break;
-          case 8: unpack_v<D, 8>(vp, stride, n, dst, hf); break;
-          default: unpack_v<D, 16>(vp, stride, n, dst, hf); break;
+        if (n == BLOCK && !drafts) {
+          const uint8_t* vp = smem + Cfg::RAW_OFF + (raw * TPAGES + pg) * page_room + v_off;
+          switch (A.vb) {
+            case 2: unpack_v<D, 2, true>(vp, D / 4, n, dst, hf); break;
+            case 4: unpack_v<D, 4, true>(vp, D / 2, n, dst, hf); break;
+            case 8: unpack_v<D, 8, true>(vp, D, n, dst, hf); break;
+            default: unpack_v<D, 16, true>(vp, 2 * D, n, dst, hf); break;
+          }
+        } else if (drafts) {
+          const __half* vp = A.v + (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
+          unpack_v<D, 16, false>(reinterpret_cast<const uint8_t*>(vp), 2 * D * (int64_t)st.Hkv, n,
+                                 dst, hf);
+        } else {  // the open block, or no tokens (zeros)
+          const uint8_t* vp =
+              n > 0 ? st.pool_base[fmt] + v_off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt]
+                    : nullptr;
+          switch (A.vb) {
+            case 2: unpack_v<D, 2, false>(vp, D / 4, n, dst, hf); break;
+            case 4: unpack_v<D, 4, false>(vp, D / 2, n, dst, hf); break;
+            case 8: unpack_v<D, 8, false>(vp, D, n, dst, hf); break;
+            default: unpack_v<D, 16, false>(vp, 2 * D, n, dst, hf); break;
+          }
         }
       }
       fence_async_smem();
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   }
   if (tid == 0) {
     for (int i = 0; i < KST; ++i) {
-      bar_init(k_full + 8 * i, TPAGES);
+      bar_init(k_full + 8 * i, TPAGES + 1);
       bar_init(k_empty + 8 * i, 1);
     }
     for (int i = 0; i < VST; ++i) {
@@ -573,11 +583,18 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     M.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  for (int i = tid; i < KST * Cfg::SUBT / 16; i += TT) {  // the 16 channels start as zeros
+    const int x = i * 16 % Cfg::SUBT;
+    *reinterpret_cast<uint4*>(smem + i * 16 / Cfg::SUBT * Cfg::KSTAGE + 2 * Cfg::OPND + x) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
   if (warp == W_SCORES) tmem_alloc(smem_u32(&M.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
-  // Columns: Q at 0 (D / 2), O at 64 (D), score buffer b of group t at 256 + 128 b + 64 t.
+  // Columns: Q at 0 (D / 2) and 192 (8), O at 64 (D), score buffer b of group t at
+  // 256 + 128 b + 64 t.
   const uint32_t tm = uniform(M.tmem);
   if (warp == 0) {             // prefix of the sequences' tiles
     int64_t run = 0;
@@ -693,6 +710,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
               for (int k = 0; k < 4; ++k)
                 mma_ts(d, tm + (y & (D / 64 - 1)) * 32 + 8 * k,
                        desc_sw128(base + y * Cfg::SUBT + k * 32, 16, 1024), ID_S, y > 0 || k > 0);
+            mma_ts(d, tm + 192, desc_sw128(base + 2 * Cfg::OPND, 16, 1024), ID_S, true);
             mma_commit(s_full + 16 * buf + 8 * t);
             mma_commit(k_empty + 8 * sg);
           }
@@ -741,16 +759,17 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       }
     } else if (warp == W_SCALES) {
       // ---- V scales and which tokens there are, two tokens a lane -------------------
-      int rs = 0, vs = 0;
-      uint32_t rph = 0, eph = 1;
+      int rs = 0, vs = 0, ks = 0;
+      uint32_t rph = 0, eph = 1, kph = 1;
       bool ok = true;
       while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
         for (int i = w.s; i < w.e; ++i) {
           const bool drafts = i == w.nt - 1;
-          ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
           ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+          ok = ok && warp_wait(k_empty + 8 * ks, kph, stop);
+          ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
           if (!ok) break;
-          int n = drafts ? min(TN, w.cnt) : min(TN, w.len - i * TN);  // tokens of the tile
+          const int n = drafts ? min(TN, w.cnt) : min(TN, w.len - i * TN);  // tokens of the tile
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int tok = lane + 32 * u, pg = tok / BLOCK, r = tok % BLOCK;
@@ -776,21 +795,36 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                 if (s == 0.f) s = 1.f;
               }
             }
-            const float inv = __fdividef(1.f, s);
-            M.lsv[vs][tok] = __log2f(s);
+            const float inv = __fdividef(1.f, s), y = __log2f(s) * A.k_ext;
             M.rsv[vs][tok] = inv;
             if (ASYM) M.zsv[vs][tok] = zv * inv;
+            // y in three fp16 parts: the first channels of the token's row (swizzled)
+            const __half h0 = __float2half_rn(y);
+            const float y1 = y - __half2float(h0);
+            const __half h1 = __float2half_rn(y1);
+            const __half h2 = __float2half_rn(y1 - __half2float(h1));
+            uint2 part;
+            part.x = __half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
+            part.y = __half_as_ushort(h2);
+            *reinterpret_cast<uint2*>(smem + ks * Cfg::KSTAGE + 2 * Cfg::OPND + tok * 128 +
+                                      ((tok & 7) << 4)) = part;
             const uint32_t bits = __ballot_sync(0xffffffffu, there);
             if (lane == 0) reinterpret_cast<uint32_t*>(M.valid[vs])[u] = bits;
           }
+          fence_async_smem();
           __syncwarp();
           if (lane == 0) {
             bar_arrive(sc_full + 8 * vs);
+            bar_arrive(k_full + 8 * ks);
             bar_arrive(raw_empty + 8 * rs);
           }
           if (++vs == VST) {
             vs = 0;
             eph ^= 1;
+          }
+          if (++ks == KST) {
+            ks = 0;
+            kph ^= 1;
           }
           if (++rs == nraw) {
             rs = 0;
@@ -815,6 +849,14 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
     int buf = 0, par = 0, tiles = 0;  // buffer; segment parity; tiles of the segments before
     bool ok = true;
     constexpr float SLACK = 8.f, BOOST = 7.f, NONE = -1e30f;
+    if (t == 0) {  // channels 0 to 2 of the 16: the constant
+      const __half2 c2 = __floats2half2_rn(A.q_ext, A.q_ext);
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(&c2);
+      const uint32_t x[16] = {c, c & 0xFFFFu};
+      tmem_st16(base + 192, x);
+      tmem_wait_st();
+      fence_before();
+    }
     while (next_seg(&M.walk[warp], M, A, st, lane, w)) {
       // This thread's row: node and query head of the group.
       const int r = w.row0 + row;
@@ -884,15 +926,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           for (int hf = 0; hf < 2; ++hf) {
             float x[32];
             tmem_ld32(ts + 32 * hf, reinterpret_cast<uint32_t*>(x));
-            const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]) + 8 * hf;
             tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {  // x + log2 s
-              const ulonglong2 a = lv[c];
-              unpack2(fma2(pack2(x[4 * c], x[4 * c + 1]), sl2, a.x), x[4 * c], x[4 * c + 1]);
-              unpack2(fma2(pack2(x[4 * c + 2], x[4 * c + 3]), sl2, a.y), x[4 * c + 2],
-                      x[4 * c + 3]);
-            }
             if (part) {
               const uint32_t bits = (uint32_t)(seen >> (32 * hf));
 #pragma unroll
@@ -903,7 +937,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             for (int c = 0; c < 32; c += 2)
               mx[c >> 1 & 3] = fmaxf(mx[c >> 1 & 3], fmaxf(x[c], x[c + 1]));
           }
-          mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * st.scale_log2;
         }
         int moves;
         asm volatile(
@@ -948,7 +982,6 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           for (int hf = 0; hf < 2; ++hf) {
             float x[32];
             tmem_ld32(ts + 32 * hf, reinterpret_cast<uint32_t*>(x));
-            const ulonglong2* lv = reinterpret_cast<const ulonglong2*>(M.lsv[sg]) + 8 * hf;
             const ulonglong2* rv = reinterpret_cast<const ulonglong2*>(M.rsv[sg]) + 8 * hf;
             const ulonglong2* zv = reinterpret_cast<const ulonglong2*>(M.zsv[sg]) + 8 * hf;
             tmem_wait_ld();
@@ -961,13 +994,11 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             uint32_t p[16];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const ulonglong2 la = lv[c], ra = rv[c];
+              const ulonglong2 ra = rv[c];
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 float a, b;
-                unpack2(fma2(pack2(x[4 * c + 2 * u], x[4 * c + 2 * u + 1]), sl2,
-                             add2(u ? la.y : la.x, off)),
-                        a, b);
+                unpack2(fma2(pack2(x[4 * c + 2 * u], x[4 * c + 2 * u + 1]), sl2, off), a, b);
                 a = ex2(a);
                 b = ex2(b);
                 const uint64_t ab = pack2(a, b);
@@ -1259,6 +1290,11 @@ extern "C" EKV_API int ekv_tree_attn(ekv_cache* cache, int32_t layer, int32_t n_
   A.ml = reinterpret_cast<float2*>(base + t.ml);
   A.pre = reinterpret_cast<int64_t*>(base + t.pre);
   A.grid = t.grid;
+  // c = 2^k near 1 / sl, so that log2 s / (sl c) is of the size of log2 s
+  const int ex = -ilogbf(st.scale_log2);
+  if (ex > 25 || ex < -14) return EKV_EUNSUPPORTED;
+  A.q_ext = ldexpf(1.f, ex > 15 ? 15 : ex);
+  A.k_ext = 1.f / (st.scale_log2 * A.q_ext);
   using Fn = cudaError_t (*)(const DevState&, TreeArgs, int, cudaStream_t);
   const Fn fn = st.D == 64 ? (st.asym ? launch_tree<64, true> : launch_tree<64, false>)
                            : (st.asym ? launch_tree<128, true> : launch_tree<128, false>);
