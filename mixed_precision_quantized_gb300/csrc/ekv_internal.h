@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ekv.h"
 
 namespace ekv {
@@ -137,6 +139,31 @@ cudaError_t launch_init_stack(int32_t* stack, int32_t n, cudaStream_t s);
 // a page); zeroes cnt first.
 cudaError_t launch_stats(const DevState& st, int l0, int nl, unsigned long long* cnt,
                          cudaStream_t s);
+
+// ---- host helpers of the serving kernels ------------------------------------------
+// SM count of the current device (looked up once a device).
+inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Allow kernel FN SMEM bytes of dynamic shared memory, once a device.
+template <auto FN, int SMEM>
+cudaError_t smem_once() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // Argument checks and launch plan of decode attention for a handle: a copy of
 // its device state, the split count and the layer's V bits.

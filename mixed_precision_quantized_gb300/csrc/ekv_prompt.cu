@@ -477,8 +477,7 @@ bool make_map(CUtensorMap* m, const void* p, int d, int heads, int64_t tokens, i
 template <int D>
 cudaError_t launch_prompt(PromptArgs A, int n_seqs, int num_sm, const CUtensorMap& mq,
                           const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(
-      prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PCfg<D>::SMEM);
+  cudaError_t e = smem_once<prompt_kernel<D>, PCfg<D>::SMEM>();
   const int32_t* cu = A.cu;
   for (int z = 0; z < n_seqs && e == cudaSuccess; z += MAX_SEQS) {
     A.cu = cu + z;
@@ -528,9 +527,8 @@ extern "C" EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, in
   A.sl = scale * 1.4426950408889634f;
   A.o = static_cast<__half*>(o);
   A.os = o_stride;
-  int dev = 0, num_sm = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&num_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  const int num_sm = sm_count();
+  if (num_sm <= 0) {
     cudaGetLastError();
     return EKV_ECUDA;
   }

@@ -75,51 +75,74 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeArgs A) {
   }
   __syncthreads();
   constexpr bool VEC = MODE < 2;
-  // Units of one head: rotated ones, then (16-byte or single-channel) copies.
+  // Units of one head: rotated ones, then (16-byte or single-channel) copies.  A thread
+  // keeps its unit and goes through the (token, head) items, q's heads before k's.
   const int ru = MODE == 0 ? A.rot / 16 : MODE == 1 ? A.rot / 8 : half;
-  const int cu = VEC ? (A.d - A.rot) / 8 : A.d - A.rot;
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int H = A.heads[which];
-    if (H == 0) continue;
-    const __half* x = A.x[which];
-    __half* y = A.y[which];
-    const int per = H * (ru + cu);
-    for (int i = tid; i < nt * per; i += ROPE_THREADS) {
-      const int t = i / per, r = i - t * per;
-      const int h = r / (ru + cu), u = r - h * (ru + cu);
-      const __half* src = x + (t0 + t) * A.xs[which] + (size_t)h * A.d;
-      __half* dst = y + (t0 + t) * A.ys[which] + (size_t)h * A.d;
-      const float2* w = s_w + t * ROPE_MAX_PAIRS;
-      if (u >= ru) {
-        const int c = A.rot + (u - ru) * (VEC ? 8 : 1);
-        if (src != dst) {
-          if (VEC) *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-          else dst[c] = src[c];
+  const int units = ru + (VEC ? (A.d - A.rot) / 8 : A.d - A.rot);
+  const int H = A.heads[0] + A.heads[1], groups = ROPE_THREADS / units;
+  const int hg = tid / units, u = tid - hg * units;
+  if (hg >= groups) return;
+  const int ia = MODE < 2 ? 8 * u : MODE == 2 ? u : 2 * u;  // first channel
+  const int ib = MODE == 0 ? half + 8 * u : MODE == 2 ? u + half : ia + 1;
+  const int ic = A.rot + (u - ru) * (VEC ? 8 : 1);
+  constexpr int N = 2;  // items in flight
+  int t[N], h[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int it = hg + i * groups;
+    t[i] = it / H;
+    h[i] = it - t[i] * H;
+  }
+  while (t[0] < nt) {
+    const __half* src[N];
+    __half* dst[N];
+    uint4 a[N], b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool k = h[i] >= A.heads[0];
+      const size_t head = (size_t)(k ? h[i] - A.heads[0] : h[i]) * A.d;
+      src[i] = (k ? A.x[1] : A.x[0]) + (t0 + t[i]) * (k ? A.xs[1] : A.xs[0]) + head;
+      dst[i] = (k ? A.y[1] : A.y[0]) + (t0 + t[i]) * (k ? A.ys[1] : A.ys[0]) + head;
+      if (t[i] >= nt) continue;
+      if (u < ru) {
+        if (VEC) a[i] = *reinterpret_cast<const uint4*>(src[i] + ia);
+        if (MODE == 0) b[i] = *reinterpret_cast<const uint4*>(src[i] + ib);
+      } else if (VEC) {
+        a[i] = *reinterpret_cast<const uint4*>(src[i] + ic);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (t[i] < nt) {
+        const float2* w = s_w + t[i] * ROPE_MAX_PAIRS + (MODE == 0 ? 8 * u : MODE == 1 ? 4 * u : u);
+        if (u >= ru) {
+          if (src[i] != dst[i]) {
+            if (VEC) *reinterpret_cast<uint4*>(dst[i] + ic) = a[i];
+            else dst[i][ic] = src[i][ic];
+          }
+        } else if (MODE == 0) {
+          rotate2(a[i].x, b[i].x, w[0], w[1]);
+          rotate2(a[i].y, b[i].y, w[2], w[3]);
+          rotate2(a[i].z, b[i].z, w[4], w[5]);
+          rotate2(a[i].w, b[i].w, w[6], w[7]);
+          *reinterpret_cast<uint4*>(dst[i] + ia) = a[i];
+          *reinterpret_cast<uint4*>(dst[i] + ib) = b[i];
+        } else if (MODE == 1) {
+          a[i].x = rotate1(a[i].x, w[0]);
+          a[i].y = rotate1(a[i].y, w[1]);
+          a[i].z = rotate1(a[i].z, w[2]);
+          a[i].w = rotate1(a[i].w, w[3]);
+          *reinterpret_cast<uint4*>(dst[i] + ia) = a[i];
+        } else {
+          const float fa = __half2float(src[i][ia]), fb = __half2float(src[i][ib]);
+          dst[i][ia] = __float2half_rn(fa * w->x - fb * w->y);
+          dst[i][ib] = __float2half_rn(fb * w->x + fa * w->y);
         }
-      } else if (MODE == 0) {
-        uint4 a = *reinterpret_cast<const uint4*>(src + 8 * u);
-        uint4 b = *reinterpret_cast<const uint4*>(src + half + 8 * u);
-        const float2* wu = w + 8 * u;
-        rotate2(a.x, b.x, wu[0], wu[1]);
-        rotate2(a.y, b.y, wu[2], wu[3]);
-        rotate2(a.z, b.z, wu[4], wu[5]);
-        rotate2(a.w, b.w, wu[6], wu[7]);
-        *reinterpret_cast<uint4*>(dst + 8 * u) = a;
-        *reinterpret_cast<uint4*>(dst + half + 8 * u) = b;
-      } else if (MODE == 1) {
-        uint4 a = *reinterpret_cast<const uint4*>(src + 8 * u);
-        const float2* wu = w + 4 * u;
-        a.x = rotate1(a.x, wu[0]);
-        a.y = rotate1(a.y, wu[1]);
-        a.z = rotate1(a.z, wu[2]);
-        a.w = rotate1(a.w, wu[3]);
-        *reinterpret_cast<uint4*>(dst + 8 * u) = a;
-      } else {
-        const int ia = MODE == 2 ? u : 2 * u, ib = MODE == 2 ? u + half : 2 * u + 1;
-        const float fa = __half2float(src[ia]), fb = __half2float(src[ib]);
-        dst[ia] = __float2half_rn(fa * w[u].x - fb * w[u].y);
-        dst[ib] = __float2half_rn(fb * w[u].x + fa * w[u].y);
+      }
+      h[i] += N * groups;
+      while (h[i] >= H) {
+        h[i] -= H;
+        ++t[i];
       }
     }
   }

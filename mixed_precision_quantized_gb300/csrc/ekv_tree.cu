@@ -1184,8 +1184,7 @@ constexpr int tree_smem() {
 
 template <int D, bool ASYM>
 cudaError_t launch_tree(const DevState& st, TreeArgs A, int n_seqs, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(
-      tree_kernel<D, ASYM>, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_smem<D>());
+  cudaError_t e = smem_once<tree_kernel<D, ASYM>, tree_smem<D>()>();
   const TreeArgs B = A;
   for (int z = 0; z < n_seqs && e == cudaSuccess; z += TSEQS) {
     A.n_seqs = n_seqs - z < TSEQS ? n_seqs - z : TSEQS;
@@ -1222,9 +1221,8 @@ struct TreeScratch {
 };
 // One CTA an SM; two partials a CTA (its first and its last segment).
 int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&t->grid, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  t->grid = sm_count();
+  if (t->grid <= 0) {
     cudaGetLastError();
     return EKV_ECUDA;
   }

@@ -75,7 +75,7 @@ __device__ __forceinline__ void load4(const float* row, int i, int n, int vec, f
 }
 
 template <int CL>
-__global__ void __launch_bounds__(VT) verify_kernel(VerifyArgs A) {
+__global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
   __shared__ int s_par[VMAX], s_tok[VMAX], s_path[VMAX], s_gone[VMAX];
   __shared__ float s_u[VMAX], s_p[VMAX], s_q[VMAX];
   __shared__ uint64_t s_wsum[VWARPS], s_part[2][CL], s_z[VMAX];
@@ -113,12 +113,19 @@ __global__ void __launch_bounds__(VT) verify_kernel(VerifyArgs A) {
     const float* pr = P + node * A.p_row;
     const float* qr = Q ? Q + node * A.q_row : nullptr;
     uint64_t sum = 0;
-    for (int t = u0; t < u1; ++t) {
-      float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-      load4(pr, t * 128 + lane * 4, V, A.vec, a);
-      if (k) load4(qr, t * 128 + lane * 4, V, A.vec, b);
+    constexpr int U = 4;  // units in flight
+    for (int t = u0; t < u1; t += U) {
+      float a[U][4], b[U][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum += residual(fix60(a[j]), fix60(b[j]), s_z, k);
+      for (int u = 0; u < U; ++u) {
+        const int n = t + u < u1 ? V : 0;
+        load4(pr, (t + u) * 128 + lane * 4, n, A.vec, a[u]);
+        load4(qr, (t + u) * 128 + lane * 4, k ? n : 0, A.vec, b[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += residual(fix60(a[u][j]), fix60(b[u][j]), s_z, k);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -326,6 +333,10 @@ extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_
   A.vec = !(((uintptr_t)target_probs | (uintptr_t)draft_probs) & 15) &&
           !((target_seq_stride | target_row_stride) & 3) &&
           (!draft_probs || !((draft_seq_stride | draft_row_stride) & 3));
-  const cudaError_t e = launch_verify<1>(A, n_seqs, reinterpret_cast<cudaStream_t>(stream));
+  // A cluster of 8 CTAs a sequence once a row has more than a few units a warp: 32
+  // sequences of 131,072 entries take 90 us with one CTA each and 9 with eight; at 1,024
+  // entries the cluster's barriers cost more than the row.
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = vocab > 8192 ? launch_verify<8>(A, n_seqs, s) : launch_verify<1>(A, n_seqs, s);
   return e == cudaSuccess ? EKV_OK : EKV_ECUDA;
 }

@@ -7,7 +7,6 @@ built, `lib()` raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -183,21 +182,39 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
+class _On:
     """Make the device (and the stream, if one is given) current, so that what the
-    binding allocates belongs to the stream the call runs on; yields its handle."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    binding allocates belongs to the stream the call runs on; gives its handle."""
+
+    __slots__ = ("stream", "ctx")
+
+    def __init__(self, device: torch.device, stream):
+        self.ctx = []
+        if device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
+        self.stream = stream
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+_on = _On
 
 
 def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device=None,
           contiguous: bool = True):
     """Check a tensor argument: type, shape (None: any extent), device, layout."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and
+            (device is None or t.device == device) and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -211,6 +228,11 @@ def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device=N
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _at(t: torch.Tensor | None):
+    """A tensor's address as ctypes takes it for a pointer argument."""
+    return None if t is None else t.data_ptr()
 
 
 def _token_stride(name: str, t: torch.Tensor) -> int:
@@ -245,6 +267,7 @@ class Cache:
         cfg.quantizer = QUANT_ASYMMETRIC if asym else QUANT_SYMMETRIC
         self.asym = bool(asym)
         self._keep = []
+        self._tree_scratch = {}  # bytes by (sequences, nodes)
         if torch_alloc:
             dev = self.device.index if self.device.index is not None else torch.cuda.current_device()
 
@@ -336,8 +359,10 @@ class Cache:
         n, H, d = seq_slots.numel(), self.num_kv_heads, self.head_dim
         dev = seq_slots.device
         _need("seq_slots", seq_slots, torch.int32, (n,))
-        _need("q", q, torch.float16, (n, None, self.num_q_heads, d), dev)
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be a tensor [n, m, Hq, d]")
         m = q.shape[1]
+        _need("q", q, torch.float16, (n, m, self.num_q_heads, d), dev)
         _need("k", k, torch.float16, (n, m, H, d), dev)
         _need("v", v, torch.float16, (n, m, H, d), dev)
         _need("parents", parents, torch.int32, (n, m), dev)
@@ -348,13 +373,16 @@ class Cache:
         with _on(dev, stream) as s:
             if out is None:
                 out = torch.empty_like(q) if n_nodes is None else torch.zeros_like(q)
-            nb = ctypes.c_int64(0)
-            _check(lib().ekv_tree_attn_scratch_bytes(self._h, n, m, ctypes.byref(nb)),
-                   "ekv_tree_attn_scratch_bytes")
-            scratch = torch.empty(max(16, nb.value), dtype=torch.uint8, device=dev)
-            _check(lib().ekv_tree_attn(self._h, layer, n, _ptr(seq_slots), m, _ptr(n_nodes),
-                                       _ptr(parents), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                       _ptr(scratch), nb.value, s), "ekv_tree_attn")
+            nb = self._tree_scratch.get((n, m))
+            if nb is None:
+                out_nb = ctypes.c_int64(0)
+                _check(lib().ekv_tree_attn_scratch_bytes(self._h, n, m, ctypes.byref(out_nb)),
+                       "ekv_tree_attn_scratch_bytes")
+                nb = self._tree_scratch[(n, m)] = out_nb.value
+            scratch = torch.empty(max(16, nb), dtype=torch.uint8, device=dev)
+            _check(lib().ekv_tree_attn(self._h, layer, n, _at(seq_slots), m, _at(n_nodes),
+                                       _at(parents), _at(q), _at(k), _at(v), _at(out),
+                                       _at(scratch), nb, s), "ekv_tree_attn")
         return out
 
     def canary_kl(self, layer: int, seq_slots: torch.Tensor, q: torch.Tensor,
@@ -542,9 +570,9 @@ class Rope:
                     outs[i] = torch.empty(ins[i].shape, dtype=torch.float16, device=dev)
                     st_out[i] = _token_stride("out", outs[i])
             heads = [0 if x is None else x.shape[1] for x in ins]
-            _check(lib().ekv_rope(ctypes.byref(self.cfg), _ptr(self.table), n, _ptr(positions),
-                                  heads[0], _ptr(ins[0]), st_in[0], _ptr(outs[0]), st_out[0],
-                                  heads[1], _ptr(ins[1]), st_in[1], _ptr(outs[1]), st_out[1], s),
+            _check(lib().ekv_rope(ctypes.byref(self.cfg), _at(self.table), n, _at(positions),
+                                  heads[0], _at(ins[0]), st_in[0], _at(outs[0]), st_out[0],
+                                  heads[1], _at(ins[1]), st_in[1], _at(outs[1]), st_out[1], s),
                    "ekv_rope")
         return outs[0], outs[1]
 
@@ -574,8 +602,8 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
             out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
         st = [_token_stride(nm, t) for nm, t in (("q", q), ("k", k), ("v", v), ("out", out))]
         _check(lib().ekv_prompt_attn(Hq, Hkv, d, float(softmax_scale), T, cu_seqlens.numel() - 1,
-                                     _ptr(cu_seqlens), _ptr(q), st[0], _ptr(k), st[1], _ptr(v),
-                                     st[2], _ptr(out), st[3], s), "ekv_prompt_attn")
+                                     _at(cu_seqlens), _at(q), st[0], _at(k), st[1], _at(v),
+                                     st[2], _at(out), st[3], s), "ekv_prompt_attn")
     return out
 
 
@@ -613,10 +641,10 @@ def verify_tree(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torch
         path = torch.empty(n, m, dtype=torch.int32, device=dev)
         n_accept = torch.empty(n, dtype=torch.int32, device=dev)
         nxt = torch.empty(n, dtype=torch.int32, device=dev)
-        _check(lib().ekv_verify_tree(n, m, V, _ptr(target_probs), strides[0], strides[1],
-                                     _ptr(draft_probs), strides[2], strides[3], _ptr(tokens),
-                                     _ptr(parents), _ptr(n_nodes), _ptr(u_accept), _ptr(u_sample),
-                                     _ptr(path), _ptr(n_accept), _ptr(nxt), s), "ekv_verify_tree")
+        _check(lib().ekv_verify_tree(n, m, V, _at(target_probs), strides[0], strides[1],
+                                     _at(draft_probs), strides[2], strides[3], _at(tokens),
+                                     _at(parents), _at(n_nodes), _at(u_accept), _at(u_sample),
+                                     _at(path), _at(n_accept), _at(nxt), s), "ekv_verify_tree")
     return path, n_accept, nxt
 
 
