@@ -139,7 +139,7 @@ struct TreeArgs {
   __half* o;
   float* acc;       // [2 grid][D / 4][128] float4
   float2* ml;       // [2 grid][128] (max, sum)
-  int64_t* pre;     // [n_seqs + 1] for the merging kernel
+  int64_t* pre;     // for the merging kernel: [n_seqs + 1], then the runs' starts [grid + 1]
   int grid;
   float q_ext, k_ext;  // Q's constant c for the log2 s channels, and 1 / (sl c)
 };
@@ -178,11 +178,13 @@ __device__ __noinline__ void walk_init(Walk* w, const TMisc& M, int n_seqs) {
   w->unit = w->nunits = 0;
 }
 // Step to the next segment (false: none).
-__device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int G, int Hkv) {
+__device__ __noinline__ bool walk_step(Walk* at, const TMisc& M, int n_seqs, int G, int Hkv) {
+  Walk v = *at;
+  Walk* const w = &v;
   while (true) {
     if (w->unit >= w->nunits) {
       const int z = ++w->z;
-      if (z >= n_seqs || M.pre[z] >= w->hi) return false;
+      if (z >= n_seqs || M.pre[z] >= w->hi) break;
       w->len = M.len[z];
       w->cnt = M.cnt[z];
       const int r = rows_of(w->cnt, G);
@@ -199,7 +201,7 @@ __device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int 
       continue;
     }
     const int64_t a = w->a;
-    if (a >= w->hi) return false;
+    if (a >= w->hi) break;
     Seg& g = w->seg;
     unit_part(a, w->nt, w->lo, w->hi, g.s, g.e);
     const int nr = row_tiles(rows_of(w->cnt, G));
@@ -212,8 +214,12 @@ __device__ __noinline__ bool walk_step(Walk* w, const TMisc& M, int n_seqs, int 
     g.slot = 2 * blockIdx.x + (w->lo > a ? 0 : 1);
     w->a = a + w->nt;
     ++w->unit;
-    if (g.s < g.e) return true;
+    if (g.s < g.e) {
+      *at = v;
+      return true;
+    }
   }
+  return false;
 }
 // By a whole warp: its next segment.
 __device__ __forceinline__ bool next_seg(Walk* wk, const TMisc& M, const TreeArgs& A,
@@ -615,8 +621,11 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       M.runs.init(run, A.grid);
     }
     __syncwarp();
-    if (blockIdx.x == 0)
+    __syncwarp();
+    if (blockIdx.x == 0) {
       for (int z = lane; z <= A.n_seqs; z += 32) A.pre[z] = M.pre[z];
+      for (int c = lane; c <= A.grid; c += 32) A.pre[A.n_seqs + 1 + c] = M.runs.start(c);
+    }
   }
   __syncthreads();
   if (lane == 0) walk_init(&M.walk[warp], M, A.n_seqs);
@@ -1096,23 +1105,18 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
                                                              int groups) {
   __shared__ int64_t s_start[MAX_GRID + 1];
   __shared__ int s_slot[MAX_GRID];
-  __shared__ Runs s_runs;
   const int rt = blockIdx.x % rt_max, h = blockIdx.x / rt_max % st.Hkv;
   const int z = blockIdx.x / rt_max / st.Hkv, row = threadIdx.x;
-  const int slot = A.slots[z];
-  const bool slot_ok = slot >= 0 && slot < st.S;
-  const int len = slot_ok ? st.len[ls_index(st, A.layer, slot)] : 0;
   const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
   const int rows = rows_of(cnt, st.G);
   if (rt * TM_ROWS >= rows) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row == 0) s_runs.init(A.pre[A.n_seqs], A.grid);
-  __syncthreads();
-  for (int i = row; i <= A.grid; i += TM_ROWS) s_start[i] = s_runs.start(i);
-  __syncthreads();
+  for (int i = row; i <= A.grid; i += TM_ROWS) s_start[i] = A.pre[A.n_seqs + 1 + i];
   // The runs that hold parts of this unit, [a, a + nt): c0 .. c1 - 1.
-  const int nt = tiles_of(len);
-  const int64_t a = A.pre[z] + (int64_t)(h * row_tiles(rows) + rt) * nt;
+  const int64_t first = A.pre[z], units = (int64_t)st.Hkv * row_tiles(rows);
+  const int nt = (int)((uint32_t)(A.pre[z + 1] - first) / (uint32_t)units);
+  const int64_t a = first + (int64_t)(h * row_tiles(rows) + rt) * nt;
+  __syncthreads();
   int c0 = 0, c1 = 0;
   for (int i0 = 0; i0 < A.grid; i0 += TM_ROWS) {
     const int i = i0 + row;
@@ -1232,7 +1236,7 @@ int tree_scratch(const DevState& st, int n_seqs, TreeScratch* t) {
   t->acc = 0;
   t->ml = parts * st.D * sizeof(float);
   t->pre = t->ml + parts * sizeof(float2);
-  t->bytes = t->pre + (size_t)(n + 1) * sizeof(int64_t);
+  t->bytes = t->pre + (size_t)(n + 1 + t->grid + 1) * sizeof(int64_t);
   return EKV_OK;
 }
 

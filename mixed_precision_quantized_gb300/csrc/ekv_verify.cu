@@ -42,13 +42,18 @@ struct VerifyArgs {
   const int32_t *tokens, *parents, *n_nodes;
   const float *u, *us;
   int32_t *path, *n_accept, *next;
-  int m, vocab, vec;
+  int m, vocab;
 };
 
-// 2^60 x for x in [0, 1] (clamped; negative and NaN: 0), truncated.
+// 2^60 x for x in [0, 1] (clamped; negative and NaN: 0), truncated: the 24-bit mantissa
+// shifted to its place (the conversion instruction to 64 bits runs at a fraction of the
+// rate of the shifts).
 __device__ __forceinline__ uint64_t fix60(float x) {
   x = x > 0.f ? fminf(x, 1.f) : 0.f;
-  return __float2ull_rz(x * 0x1p60f);
+  const uint32_t bits = __float_as_uint(x);
+  const int up = (int)(bits >> 23) - 90;  // x = m 2^(e - 150)
+  const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u;
+  return up >= 0 ? m << up : up > -24 ? m >> -up : 0;
 }
 // a * z in units of 2^-60, a < 2^62 and z < 2^62 (saturated by the caller).
 __device__ __forceinline__ uint64_t mul60(uint64_t a, uint64_t z) {
@@ -64,20 +69,29 @@ __device__ __forceinline__ uint64_t residual(uint64_t r, uint64_t q, const uint6
   return r;
 }
 
-__device__ __forceinline__ void load4(const float* row, int i, int n, int vec, float* f) {
-  if (vec && i + 4 <= n) {
+// Entries i .. i + 3 of a row of n (zero outside it), as one load where they lie inside
+// and on a 16-byte boundary.
+__device__ __forceinline__ void load4(const float* row, int i, int n, float* f) {
+  if (i >= 0 && i + 4 <= n && !(reinterpret_cast<uintptr_t>(row + i) & 15)) {
     const float4 t = *reinterpret_cast<const float4*>(row + i);
     f[0] = t.x; f[1] = t.y; f[2] = t.z; f[3] = t.w;
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = i + j < n ? row[i + j] : 0.f;
+    for (int j = 0; j < 4; ++j) f[j] = i + j >= 0 && i + j < n ? row[i + j] : 0.f;
   }
+}
+// Entries by which a row starts behind a 16-byte boundary: its units begin that much
+// before it, so that any row (an odd vocabulary) is read in aligned vectors.
+__device__ __forceinline__ int lead(const float* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
 }
 
 template <int CL>
-__global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
-  __shared__ int s_par[VMAX], s_tok[VMAX], s_path[VMAX], s_gone[VMAX];
+__global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
+  __shared__ int s_par[VMAX], s_tok[VMAX], s_path[VMAX], s_gone[VMAX], s_first[VMAX], s_ngone;
   __shared__ float s_u[VMAX], s_p[VMAX], s_q[VMAX];
+  __shared__ bool s_twin[VMAX], s_ok[VMAX];
+  __shared__ unsigned long long s_kids[VMAX];
   __shared__ uint64_t s_wsum[VWARPS], s_part[2][CL], s_z[VMAX];
   const int z = blockIdx.x / CL, rank = blockIdx.x % CL;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,22 +99,50 @@ __global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
   const int cnt = A.n_nodes ? min(A.m, A.n_nodes[z]) : A.m;
   const float* P = A.p + z * A.p_seq;
   const float* Q = A.q ? A.q + z * A.q_seq : nullptr;
-  if (tid < cnt) {
-    const int par = tid ? A.parents[(size_t)z * A.m + tid] : -1;
-    const int tok = A.tokens[(size_t)z * A.m + tid];
-    // a bad parent or a token outside the vocabulary: no one's child
-    const bool ok = tid > 0 && par >= 0 && par < tid && tok >= 0 && tok < V;
-    s_par[tid] = ok ? par : -1;
-    s_tok[tid] = tok;
-    s_u[tid] = A.u[(size_t)z * A.m + tid];
-    s_p[tid] = ok ? P[par * A.p_row + tok] : 0.f;
-    s_q[tid] = ok && Q ? Q[par * A.q_row + tok] : 1.f;
+  if (tid < VMAX) {
+    s_par[tid] = -1;
+    s_first[tid] = VMAX;
+    s_kids[tid] = 0;
+    if (tid == 0) s_ngone = 0;
+    if (tid < cnt) {
+      const int par = tid ? A.parents[(size_t)z * A.m + tid] : -1;
+      const int tok = A.tokens[(size_t)z * A.m + tid];
+      // a bad parent or a token outside the vocabulary: no one's child
+      const bool ok = tid > 0 && par >= 0 && par < tid && tok >= 0 && tok < V;
+      s_par[tid] = ok ? par : -1;
+      s_tok[tid] = tok;
+      s_u[tid] = A.u[(size_t)z * A.m + tid];
+      s_p[tid] = ok ? P[par * A.p_row + tok] : 0.f;
+      s_q[tid] = ok && Q ? Q[par * A.q_row + tok] : 1.f;
+    }
+  }
+  __syncthreads();
+  const int par = tid < cnt ? s_par[tid] : -1;
+  if (par >= 0) atomicOr(&s_kids[par], 1ull << tid);
+  __syncthreads();
+  const unsigned long long before = par >= 0 ? s_kids[par] & ((1ull << tid) - 1) : 0;
+  if (par >= 0) {
+    bool twin = false;  // an earlier sibling has the same token
+    for (unsigned long long x = before; x; x &= x - 1) twin |= s_tok[__ffsll(x) - 1] == s_tok[tid];
+    s_twin[tid] = twin;
+  }
+  __syncthreads();
+  if (par >= 0 && Q) s_ok[tid] = (double)s_u[tid] * (double)s_q[tid] < (double)s_p[tid];
+  if (par >= 0 && !Q && !s_twin[tid]) {
+    // Without draft probabilities every node's test is known at once: Z is 1 less the
+    // mass of its earlier siblings (each token once).
+    double left = 1.0;
+    for (unsigned long long x = before; x; x &= x - 1) {
+      const int j = __ffsll(x) - 1;
+      if (!s_twin[j]) left -= (double)s_p[j];
+    }
+    if ((double)s_u[tid] * left < (double)s_p[tid]) atomicMin(&s_first[par], tid);
   }
   __syncthreads();
 
   // The slice of a row that this CTA sums, and each warp's chunk of it, in units
   // of 128 elements (one 16-byte load per lane): contiguous, in order.
-  const int units = (V + 127) / 128;
+  const int units = (V + 3 + 127) / 128;  // with the lead of a row
   const int per_warp = (units + CL * VWARPS - 1) / (CL * VWARPS);
   const int u0 = min(units, (rank * VWARPS + warp) * per_warp);
   const int u1 = min(units, u0 + per_warp);
@@ -113,26 +155,45 @@ __global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
     const float* pr = P + node * A.p_row;
     const float* qr = Q ? Q + node * A.q_row : nullptr;
     uint64_t sum = 0;
-    constexpr int U = 4;  // units in flight
-    for (int t = u0; t < u1; t += U) {
-      float a[U][4], b[U][4];
+    // Short loops on purpose: each row is passed once or twice a launch, and code that is
+    // run so seldom costs its instruction fetches (unrolled over 4 units a pass took 7 us).
+    float a[4], b[4];
+    const int at = lane * 4 - lead(pr);
+    load4(pr, u0 * 128 + at, u0 < u1 ? V : 0, a);
+    if (k == 0) {
+#pragma unroll 1
+      for (int t = u0; t < u1; ++t) {
+        float c[4];
+        load4(pr, (t + 1) * 128 + at, t + 1 < u1 ? V : 0, c);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = t + u < u1 ? V : 0;
-        load4(pr, (t + u) * 128 + lane * 4, n, A.vec, a[u]);
-        load4(qr, (t + u) * 128 + lane * 4, k ? n : 0, A.vec, b[u]);
+        for (int j = 0; j < 4; ++j) {
+          sum += fix60(a[j]);
+          a[j] = c[j];
+        }
       }
+    } else {
+      load4(qr, u0 * 128 + at, u0 < u1 ? V : 0, b);
+#pragma unroll 1
+      for (int t = u0; t < u1; ++t) {
+        float c[4], d[4];
+        load4(pr, (t + 1) * 128 + at, t + 1 < u1 ? V : 0, c);
+        load4(qr, (t + 1) * 128 + at, t + 1 < u1 ? V : 0, d);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum += residual(fix60(a[u][j]), fix60(b[u][j]), s_z, k);
+        for (int j = 0; j < 4; ++j) {
+          // (what p <= q leaves after one rejection stays zero after more)
+          if (a[j] > b[j] || b[j] != b[j]) sum += k == 1 ? fix60(a[j]) - fix60(b[j])
+                                                        : residual(fix60(a[j]), fix60(b[j]), s_z, k);
+          a[j] = c[j];
+          b[j] = d[j];
+        }
+      }
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if (lane == 0) s_wsum[warp] = sum;
     __syncthreads();
     if (tid < ngone) {  // distinct tokens, each in one warp's chunk
-      const int x = s_gone[tid], w = x / 128 / per_warp - rank * VWARPS;
+      const int x = s_gone[tid], w = (x + lead(pr)) / 128 / per_warp - rank * VWARPS;
       if (w >= 0 && w < VWARPS)
         atomicAdd(reinterpret_cast<unsigned long long*>(&s_wsum[w]),
                   (unsigned long long)(0 - fix60(pr[x])));
@@ -156,48 +217,43 @@ __global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
   int node = 0, nacc = 0, k = 0, ngone = 0;
   uint64_t total = 0;
   bool have = false;  // `total` is the residual's sum at the current node
-  if (cnt > 0) {
+  if (cnt > 0 && !Q) {
+    for (int c; (c = s_first[node]) < VMAX; node = c) {
+      if (tid == 0) s_path[nacc] = c;
+      ++nacc;
+    }
+    // the tokens that the last node's rejected children took out
+    if (par == node && !s_twin[tid]) s_gone[atomicAdd(&s_ngone, 1)] = s_tok[tid];
+    __syncthreads();
+    ngone = s_ngone;
+  } else if (cnt > 0) {
     double left = 1.0;
-    for (int c = 1; c < cnt; ++c) {
-      if (s_par[c] != node) continue;
-      const int x = s_tok[c];
-      double r;
-      if (!Q) {
-        bool twin = false;
-        for (int j = 0; j < ngone; ++j) twin |= s_gone[j] == x;
-        r = twin ? 0.0 : (double)s_p[c];
-      } else {
-        r = k == 0 ? (double)s_p[c]
-                   : (double)residual(fix60(s_p[c]), fix60(s_q[c]), s_z, k) * 0x1p-60;
-      }
-      if ((double)s_u[c] * (double)s_q[c] * left < r) {
+    unsigned long long kids = s_kids[0];
+    while (kids) {
+      const int c = __ffsll(kids) - 1;
+      kids &= kids - 1;
+      // (a first child's test, r = p and Z = 1, was made for all nodes at once)
+      const bool take =
+          k == 0 ? s_ok[c]
+                 : (double)s_u[c] * (double)s_q[c] * left <
+                       (double)residual(fix60(s_p[c]), fix60(s_q[c]), s_z, k) * 0x1p-60;
+      if (take) {
         if (tid == 0) s_path[nacc] = c;
         ++nacc;
         node = c;
-        k = ngone = 0;
+        kids = s_kids[c];
+        k = 0;
         left = 1.0;
         have = false;
         continue;
       }
-      if (!Q) {
-        left -= r;
-        bool twin = false;
-        for (int j = 0; j < ngone; ++j) twin |= s_gone[j] == x;
-        if (!twin) {
-          __syncthreads();
-          if (tid == 0) s_gone[ngone] = x;
-          ++ngone;
-          __syncthreads();
-        }
-      } else {
-        __syncthreads();
-        if (tid == 0) s_z[k] = k == 0 ? 1ull << 60 : min(total, (uint64_t)((1ull << 62) - 1));
-        ++k;
-        __syncthreads();
-        total = row_sum(node, k, 0);
-        have = true;
-        left = (double)total * 0x1p-60;
-      }
+      __syncthreads();
+      if (tid == 0) s_z[k] = k == 0 ? 1ull << 60 : min(total, (uint64_t)((1ull << 62) - 1));
+      ++k;
+      __syncthreads();
+      total = row_sum(node, k, 0);
+      have = true;
+      left = (double)total * 0x1p-60;
     }
   }
 
@@ -220,21 +276,26 @@ __global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
       if (target >= base && target - base < s_wsum[warp]) {  // this warp's chunk holds it
         const float* pr = P + node * A.p_row;
         const float* qr = Q ? Q + node * A.q_row : nullptr;
+#pragma unroll 1
         for (int t = u0; t < u1; ++t) {
           float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-          const int i0 = t * 128 + lane * 4;
-          load4(pr, i0, V, A.vec, a);
-          if (k) load4(qr, i0, V, A.vec, b);
+          const int i0 = t * 128 + lane * 4 - lead(pr);
+          load4(pr, i0, V, a);
+          if (k) load4(qr, i0, V, b);
           uint64_t e[4], s = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            e[j] = residual(fix60(a[j]), fix60(b[j]), s_z, k);
-            for (int g = 0; g < ngone; ++g)
-              if (s_gone[g] == i0 + j) e[j] = 0;
-            s += e[j];
-          }
-          uint64_t inc = s;
+          for (int j = 0; j < 4; ++j) e[j] = residual(fix60(a[j]), fix60(b[j]), s_z, k);
+#pragma unroll 1
+          for (int g = 0; g < ngone; ++g) {
+            const int at = s_gone[g] - i0;
 #pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (at == j) e[j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s += e[j];
+          uint64_t inc = s;
+#pragma unroll 1
           for (int off = 1; off < 32; off <<= 1) {
             const uint64_t o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
@@ -243,13 +304,13 @@ __global__ void __launch_bounds__(VT, 1) verify_kernel(VerifyArgs A) {
           if (hit) {
             if (lane == __ffs(hit) - 1) {
               uint64_t cum = base + inc - s;
+              int at = i0;
+#pragma unroll
               for (int j = 0; j < 4; ++j) {
                 cum += e[j];
-                if (cum > target) {
-                  A.next[z] = i0 + j;
-                  break;
-                }
+                at += cum <= target;
               }
+              A.next[z] = at;
             }
             break;
           }
@@ -330,9 +391,6 @@ extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_
   A.next = next_token;
   A.m = max_nodes;
   A.vocab = vocab;
-  A.vec = !(((uintptr_t)target_probs | (uintptr_t)draft_probs) & 15) &&
-          !((target_seq_stride | target_row_stride) & 3) &&
-          (!draft_probs || !((draft_seq_stride | draft_row_stride) & 3));
   // A cluster of 8 CTAs a sequence once a row has more than a few units a warp: 32
   // sequences of 131,072 entries take 90 us with one CTA each and 9 with eight; at 1,024
   // entries the cluster's barriers cost more than the row.

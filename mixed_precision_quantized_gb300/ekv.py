@@ -184,9 +184,9 @@ def _stream(stream) -> ctypes.c_void_p:
 
 class _On:
     """Make the device (and the stream, if one is given) current, so that what the
-    binding allocates belongs to the stream the call runs on; gives its handle."""
+    binding allocates belongs to the stream the call runs on."""
 
-    __slots__ = ("stream", "ctx")
+    __slots__ = ("ctx",)
 
     def __init__(self, device: torch.device, stream):
         self.ctx = []
@@ -194,19 +194,36 @@ class _On:
             self.ctx.append(torch.cuda.device(device))
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
-        self.stream = stream
 
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
 
 
-_on = _On
+class _Here:
+    """The same where the device is current already and no stream is given."""
+
+    __slots__ = ("handle",)
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _on(device: torch.device, stream):
+    index = torch.cuda.current_device()
+    if stream is not None or device.index != index:
+        return _On(device, stream)
+    h = _Here()
+    h.handle = torch._C._cuda_getCurrentRawStream(index)
+    return h
 
 
 def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device=None,
@@ -238,9 +255,10 @@ def _at(t: torch.Tensor | None):
 def _token_stride(name: str, t: torch.Tensor) -> int:
     """Token stride (elements) of [tokens, heads, d] whose heads are contiguous."""
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else max(h * d, 8)
+    return st[0] if n > 1 else max(h * d, 8)
 
 
 class Cache:
@@ -543,6 +561,7 @@ class Rope:
             self.device = torch.device("cuda", torch.cuda.current_device())
         signed = [t - (1 << 64) if t >= 1 << 63 else t for t in self.turns]
         self.table = torch.tensor(signed, dtype=torch.int64, device=self.device)
+        self._cfg, self._table = ctypes.byref(self.cfg), self.table.data_ptr()
 
     def __call__(self, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
                  q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
@@ -550,31 +569,32 @@ class Rope:
         """(q_out, k_out): q [n, Hq, d] and k [n, Hkv, d] (either may be None) turned to
         positions [n] int32.  Token strides are free (views of a fused projection),
         the heads of a token contiguous; q_out / k_out may be q / k (in place)."""
-        d, n, dev = self.cfg.head_dim, positions.numel(), self.device
+        n, dev = positions.numel(), self.device
         _need("positions", positions, torch.int32, (n,), dev)
-        ins, outs, st_in, st_out = [q, k], [q_out, k_out], [0, 0], [0, 0]
-        for i, name in enumerate("qk"):
-            if ins[i] is None:
-                if outs[i] is not None:
-                    raise ValueError(f"{name}_out without {name}")
-                continue
-            _need(name, ins[i], torch.float16, (n, None, d), dev, contiguous=False)
-            st_in[i] = _token_stride(name, ins[i])
-            if outs[i] is not None:
-                _need(name + "_out", outs[i], torch.float16, tuple(ins[i].shape), dev,
-                      contiguous=False)
-                st_out[i] = _token_stride(name + "_out", outs[i])
         with _on(dev, stream) as s:
-            for i in range(2):
-                if ins[i] is not None and outs[i] is None:
-                    outs[i] = torch.empty(ins[i].shape, dtype=torch.float16, device=dev)
-                    st_out[i] = _token_stride("out", outs[i])
-            heads = [0 if x is None else x.shape[1] for x in ins]
-            _check(lib().ekv_rope(ctypes.byref(self.cfg), _at(self.table), n, _at(positions),
-                                  heads[0], _at(ins[0]), st_in[0], _at(outs[0]), st_out[0],
-                                  heads[1], _at(ins[1]), st_in[1], _at(outs[1]), st_out[1], s),
+            q_out, qa = self._side("q", q, q_out, n)
+            k_out, ka = self._side("k", k, k_out, n)
+            _check(lib().ekv_rope(self._cfg, self._table, n, positions.data_ptr(), *qa, *ka, s),
                    "ekv_rope")
-        return outs[0], outs[1]
+        return q_out, k_out
+
+    def _side(self, name: str, x, out, n: int):
+        """One tensor's output and its arguments: heads, address, stride, of the output too."""
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            return None, (0, None, 0, None, 0)
+        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+            raise ValueError(f"{name} must be a tensor [tokens, heads, d]")
+        h, d = x.shape[1], self.cfg.head_dim
+        shape = (n, h, d)
+        _need(name, x, torch.float16, shape, self.device, contiguous=False)
+        if out is None:
+            out, st = torch.empty(shape, dtype=torch.float16, device=self.device), h * d
+        else:
+            _need(name + "_out", out, torch.float16, shape, self.device, contiguous=False)
+            st = _token_stride(name + "_out", out)
+        return out, (h, x.data_ptr(), _token_stride(name, x), out.data_ptr(), st)
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
