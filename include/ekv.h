@@ -487,12 +487,15 @@ EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t 
  *               empty); rows outside every sequence are neither used nor written
  *   q, o        dev fp16, token t's heads at q + t * q_stride, [Hq][d] contiguous
  *   k, v        the same with [Hkv][d]; strides in elements, multiples of 8, at
- *               least a token's heads; bases 16-byte aligned
+ *               least a token's heads; bases 16-byte aligned; o overlaps none of q, k, v
  * o_ih = sum_{j <= i} softmax_j(scale q_ih . k_jg) v_jg over i's sequence,
  * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d).  fp32 accumulation, the
  * probabilities rounded to fp16 before they multiply V, o rounded to fp16 (RNE).
  * head_dim 64 or 128 (else EKV_EUNSUPPORTED).  total_tokens: rows of every
- * buffer; bounds outside [0, total_tokens] or descending leave that sequence out. */
+ * buffer; bounds outside [0, total_tokens] or descending leave that sequence out.
+ * The call keeps no state and takes no scratch: calls may overlap on the GPU.  A
+ * bounded wait inside the kernel that gave up (it never should) leaves NaN in the
+ * rows it was to write. */
 EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                             float softmax_scale, int32_t total_tokens, int32_t n_seqs,
                             const int32_t* cu_seqlens, const void* q, int64_t q_stride,
@@ -514,8 +517,10 @@ EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_
  * its ancestors.  A sequence may have no cached tokens.  The handle's softmax scale
  * times log2(e) lies in [2^-25, 2^15), else EKV_EUNSUPPORTED.
  *   scratch    dev, 16-byte aligned, ekv_tree_attn_scratch_bytes bytes
- *              (caller-owned; overwritten; one call at a time)
- * Device errors as ekv_decode_attn. */
+ *              (caller-owned; overwritten; one call at a time.  Nothing of the handle
+ *              is written but its error word, so calls with scratches of their own may
+ *              overlap with one another and with decode attention)
+ * Device errors as ekv_decode_attn.  Equal calls give equal bits. */
 #define EKV_TREE_MAX_NODES 64
 EKV_API int ekv_tree_attn(ekv_cache* cache, int32_t layer, int32_t n_seqs,
                           const int32_t* seq_slots, int32_t max_nodes, const int32_t* n_nodes,

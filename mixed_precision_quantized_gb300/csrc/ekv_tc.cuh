@@ -152,6 +152,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      EKV_I8(r, 0)
+      : "memory");
+}
+
 // ---- MMA -------------------------------------------------------------------------
 // Descriptor of an operand in shared memory, 128-byte swizzle.  K-major (rows of the
 // operand are rows of the tile): `sbo` 1024 between groups of 8 rows, `lbo` unused.

@@ -11,34 +11,42 @@
 // (1 to 512), so each page is worth 16 keys to all of them: it is read from memory and
 // unpacked once, and the products go to tcgen05 with 128 rows as M.  Tokens are taken in
 // tiles of 64 (4 pages); the drafted nodes are one more tile of raw fp16 rows.  Roles:
-//   warp 25      page copies (cp.async.bulk) into a ring of raw tiles
-//   warps 8-23   two sets that take the tiles in turn: unpack the K (8, 9, 12, 13) and the
-//                V parts of a raw tile, a page a warp (K and V on different schedulers: less
-//                code for each), into swizzled fp16 operand tiles: K as hi + lo
+//   warp 17      page copies (cp.async.bulk) into a ring of raw tiles
+//   warps 8-15   unpack a raw tile into swizzled fp16 operand tiles, a page's K or V a warp
+//                (K on schedulers 0 and 1, V on 2 and 3: less code for each): K as hi + lo
 //                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K need
 //                hi alone), V as the bare codes (exact in fp16)
-//   warp 26      the V scales of a tile, for softmax
-//   warps 24, 27 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
+//   warp 18      the V scales of a tile, for softmax
+//   warps 16, 19 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
 //                their waits in one loop took longer than the products)
 //   warps 0-3, 4-7  softmax, one row a thread; the two groups take the even and the odd
-//                token tiles of a pair, for the same rows
-// What bounds it at few rows is the chain of waits from scores to probabilities to
-// products, ~2,500 cycles; so scores run up to two pairs ahead (four score buffers in
-// tensor memory), with one accumulator and one running reference for both groups: before
-// the exponentials of a pair a barrier with an OR over the 256 threads tells whether any
-// row's reference has to move, which is seldom.
+//                token tiles of a pair, for the same rows.  Scores run up to two pairs ahead
+//                (four score buffers in tensor memory), with one accumulator and one running
+//                reference for both groups: before the exponentials of a pair a barrier with
+//                an OR over the 256 threads tells whether any row's reference has to move,
+//                which is seldom.
+//
+// What bounds it is instruction issue: a 64-token tile takes about 4,500 warp instructions
+// (K 1,000, V 500, softmax 1,200 at 128 rows, the rest waits and bookkeeping of the roles)
+// at 0.6 a cycle and scheduler, while the tensor cores are busy a quarter of the time and
+// DRAM a fifth.  Measured at 131,072 tokens, 8 KV heads, 128 rows, 4-bit K and V: 119 us
+// with the merging kernel (154 MB: 1.29 TB/s).  Tried and slower: 16 unpacking warps (128 us: more
+// waits to issue), half a page a warp (136), unrolled unpacking or softmax loops (121, 124:
+// the code of 20 warps in different roles outgrows the instruction caches; the stall for
+// instructions was the largest of all until the loops were short), V scales read by each
+// softmax thread from shared memory (140), polling waits without a suspend hint (203).
 //
 // A token's V scale s multiplies its probability: P' = 2^(x + log2 s - m) in fp16, where
 // the reference m follows the largest x + log2 s, so the fp16 range is used well whatever
 // the scales; the row sum adds P' / s in fp32.  The log2 s come with the scores: 16 more
 // channels of K hold log2 s / (sigma log2 e) as three fp16 parts, against a constant in Q
 // (each softmax thread loading 64 of them twice from shared memory took longer than the
-// exponentials).  As in prompt attention m moves only for
-// a gain above 2^8, P' carries 2^7, and P' is the one value rounded to fp16.
+// exponentials).  As in prompt attention m moves only for a gain above 2^8, P' carries
+// 2^7, and P' is the one value rounded to fp16.
 //
 // Work split: the token tiles of all (sequence, KV head, row tile) units laid end to end,
-// cut into equal runs, one per CTA (one CTA an SM); a run may hold parts of
-// several units.  A unit cut by run ends leaves fp32 partials (numerator, max, sum) in
+// cut into equal runs, one per CTA (one CTA an SM); a run may hold parts of several
+// units.  A unit cut by run ends leaves fp32 partials (numerator, max, sum) in
 // the scratch, and a second small kernel merges them by log-sum-exp.  The cut depends on
 // the lengths only, so equal calls give equal bits.
 #include <math_constants.h>
@@ -54,10 +62,8 @@ using namespace tc;
 constexpr int TM_ROWS = 128;      // rows of a row tile
 constexpr int TN = 64;            // tokens of a token tile
 constexpr int TPAGES = TN / BLOCK;
-constexpr int TT = 896;           // threads
-constexpr int SETS = 2;           // sets of unpacking warps, taking the tiles in turn
-constexpr int W_SCORES = 8 + 8 * SETS, W_PAGES = W_SCORES + 1, W_SCALES = W_SCORES + 2,
-              W_VALUES = W_SCORES + 3;
+constexpr int TT = 640;           // threads (96 registers each)
+constexpr int W_SCORES = 16, W_PAGES = 17, W_SCALES = 18, W_VALUES = 19;  // single-warp roles
 constexpr int TSEQS = 256;        // sequences of one launch
 constexpr int KST = 2;            // K operand tiles in flight (each free once its scores are)
 constexpr int VST = 4;            // V operand tiles in flight (until their products are done)
@@ -85,11 +91,10 @@ struct Runs {
   }
   __device__ int64_t start(int c) const { return quot * c + rest * c / grid; }
 };
-// Raw tiles in flight for pages of `room` bytes: an even number, so that each ring slot is
-// always the same unpacking set's (a set that skipped a slot's use could take the phase
-// before for its own).  The drafts' tile takes a slot too, without copies.
+// Raw tiles in flight for pages of `room` bytes.  (The drafts' tile takes a slot too,
+// without copies.)
 __device__ __forceinline__ int raw_tiles(int room) {
-  return min(RAW_MAX, RAW_BYTES / (TPAGES * room)) / SETS * SETS;
+  return min(RAW_MAX, RAW_BYTES / (TPAGES * room));
 }
 
 // A segment: the token tiles s .. e-1 of one unit.
@@ -457,15 +462,16 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
   const int nraw = raw_tiles(page_room);
   const int pg = (warp & 1) + (warp >> 1 & 2);  // page of the tile
   const Lane<D> hf(lane);
-  const int set = (warp >> 3) - 1;
-  int rs = 0, sg = 0, turn = 0;
+  int rs = 0, sg = 0;
   uint32_t rph = 0, eph = 1;
   bool ok = true;
   while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
     for (int i = w.s; i < w.e; ++i) {
       const bool drafts = i == w.nt - 1;
       const int at = sg, raw = rs;
-      const uint32_t full_phase = rph, empty_phase = eph;
+      ok = ok && warp_wait(out_empty + 8 * sg, eph, stop);
+      ok = ok && warp_wait(raw_full + 8 * rs, rph, stop);
+      if (!ok) break;
       if (++sg == (IS_K ? KST : VST)) {
         sg = 0;
         eph ^= 1;
@@ -474,12 +480,6 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
         rs = 0;
         rph ^= 1;
       }
-      const bool other = turn != set;  // another set's tile
-      if (++turn == SETS) turn = 0;
-      if (other) continue;
-      ok = ok && warp_wait(out_empty + 8 * at, empty_phase, stop);
-      ok = ok && warp_wait(raw_full + 8 * raw, full_phase, stop);
-      if (!ok) break;
       uint8_t* dst = smem + pg * BLOCK * 128 +
                      (IS_K ? at * Cfg::KSTAGE : Cfg::V_OFF + at * Cfg::OPND);
       // Where the part's rows are and how many hold tokens: in the raw tile; the open

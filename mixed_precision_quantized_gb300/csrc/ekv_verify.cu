@@ -181,8 +181,10 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // (what p <= q leaves after one rejection stays zero after more)
-          if (a[j] > b[j] || b[j] != b[j]) sum += k == 1 ? fix60(a[j]) - fix60(b[j])
-                                                        : residual(fix60(a[j]), fix60(b[j]), s_z, k);
+          if (a[j] > b[j] || b[j] != b[j]) {
+            const uint64_t x = fix60(a[j]), y = fix60(b[j]);
+            sum += k == 1 ? x - y : residual(x, y, s_z, k);
+          }
           a[j] = c[j];
           b[j] = d[j];
         }
@@ -395,6 +397,7 @@ extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_
   // sequences of 131,072 entries take 90 us with one CTA each and 9 with eight; at 1,024
   // entries the cluster's barriers cost more than the row.
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = vocab > 8192 ? launch_verify<8>(A, n_seqs, s) : launch_verify<1>(A, n_seqs, s);
+  const cudaError_t e =
+      vocab > 8192 ? launch_verify<8>(A, n_seqs, s) : launch_verify<1>(A, n_seqs, s);
   return e == cudaSuccess ? EKV_OK : EKV_ECUDA;
 }

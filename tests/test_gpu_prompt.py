@@ -73,6 +73,37 @@ def test_many_sequences():
     _check(q, k, v, o, cu)
 
 
+def test_more_sequences_than_one_launch_takes():
+    """1,100 sequences of 0 to 5 tokens (a launch takes 512)."""
+    lens = np.random.default_rng(1).integers(0, 6, 1100).tolist()
+    q, k, v = _inputs(sum(lens), 2, 1, 64)
+    cu = [0, *np.cumsum(lens).tolist()]
+    o = ekv.prompt_attn(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    _check(q, k, v, o, cu)
+
+
+def test_offsets_past_32_bits():
+    """Token strides of 2^20 elements over 4,200 tokens: the last rows lie 4.4e9 elements
+    behind the first."""
+    T, step = 4200, 1 << 20
+    bufs = [torch.empty(T, step, dtype=torch.float16, device="cuda") for _ in range(2)]
+    q, k, v = _inputs(T, 2, 1, 64, seed=2)
+    bufs[0][:, :128] = q.view(T, 128)
+    bufs[0][:, 128:192] = k.view(T, 64)
+    bufs[0][:, 256:320] = v.view(T, 64)
+    view = lambda b, c, h: b[:, c:c + 64 * h].unflatten(1, (h, 64))  # noqa: E731
+    cu = torch.tensor([0, 100, 4090, T], dtype=torch.int32, device="cuda")
+    o = ekv.prompt_attn(view(bufs[0], 0, 2), view(bufs[0], 128, 1), view(bufs[0], 256, 1), cu,
+                        out=view(bufs[1], 0, 2))
+    want = ekv.prompt_attn(q, k, v, cu)
+    assert torch.equal(o, want)
+    _check(q[4090:], k[4090:], v[4090:], o[4090:], [0, T - 4090])
+    rope = ekv.Rope(64)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    qo, _ = rope(view(bufs[0], 0, 2), None, pos, q_out=view(bufs[1], 0, 2))
+    assert torch.equal(qo, rope(q, None, pos)[0])
+
+
 def test_rows_behind_and_before_the_sequences_are_left_and_never_read():
     """A padded buffer: rows outside the sequences hold NaN and infinities, and the
     output keeps what it held there."""

@@ -195,6 +195,63 @@ def test_zero_values_beside_large_logits(case):
     c.check(o, q, kd, vd, par)
 
 
+def test_more_sequences_than_one_launch_takes(case):
+    """300 sequences of 0 to 40 tokens (a launch takes 256)."""
+    lens = np.random.default_rng(2).integers(0, 41, 300).tolist()
+    c = case(lens, 2, 1, 64, [4], 8)
+    c.run(3, cnt=np.random.default_rng(3).integers(0, 4, 300).tolist())
+
+
+def test_the_same_sequence_twice_and_equal_bits(case):
+    """A slot listed twice gives the same rows twice; repeated calls, and calls that
+    overlap on two streams, give equal bits."""
+    c = case([1500, 600], 8, 2, 128, [4, 2], 4)
+    q, k, v, par = c.drafts(9)
+    q[1], k[1], v[1], par[1] = q[0], k[0], v[0], par[0]
+    dp = torch.from_numpy(par).cuda()
+    twice = torch.zeros(2, dtype=torch.int32, device="cuda")
+    a = c.cache.tree_attn(0, twice, q, k, v, dp)
+    c.cache.sync()
+    c.state[1], c.lens = c.state[0], [1500, 1500]
+    c.check(a, q, k, v, par)
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    for s in ss:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [c.cache.tree_attn(0, twice, q, k, v, dp, stream=ss[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) for o in outs)
+
+
+@pytest.mark.parametrize("scale,ok", [(1e-6, True), (0.01, True), (3.0, True), (900.0, True),
+                                      (1e-9, False), (1e6, False)])
+def test_softmax_scales(scale, ok):
+    """The handle's own scale, from one that makes every weight equal to one that leaves
+    the largest alone; outside the stated range the call is refused."""
+    rng = np.random.default_rng(5)
+    cache = ekv.Cache(1, 1, 4, 2, 64, 64, {(8, 8): 16}, [8], [8], softmax_scale=scale)
+    st = SeqState(2, 64, 8, None, None, False)
+    k, v = (rng.normal(size=(50, 2, 64)).astype(np.float16) for _ in range(2))
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache.append(0, slots, torch.from_numpy(k[None]).cuda(), torch.from_numpy(v[None]).cuda())
+    st.append(k, v, 8)
+    q, kd, vd = (torch.from_numpy(rng.normal(size=(1, 3, h, 64)).astype(np.float16)).cuda()
+                 for h in (4, 2, 2))
+    par = torch.tensor([[-1, 0, 0]], dtype=torch.int32, device="cuda")
+    if ok:
+        o = cache.tree_attn(0, slots, q, kd, vd, par)
+        cache.sync()
+        want, tol = serving.attention(
+            q[0].cpu().numpy(), np.concatenate([st.khat(), kd[0].cpu().numpy()]),
+            np.concatenate([st.vhat(), vd[0].cpu().numpy()]),
+            serving.tree_sees([-1, 0, 0], 3, 50), np.float32(scale))
+        assert np.all(np.abs(o[0].double().cpu().numpy() - want) <= tol)
+    else:
+        with pytest.raises(ekv.EkvError) as e:
+            cache.tree_attn(0, slots, q, kd, vd, par)
+        assert e.value.code == EUNSUPPORTED
+    cache.close()
+
+
 def test_one_node_equals_the_decode_step():
     """A tree of one node over the cache is the decode step's attention: append the
     node on a twin and read it back through ekv_append_decode_attn (the newest token
