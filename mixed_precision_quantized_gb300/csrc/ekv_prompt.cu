@@ -25,6 +25,14 @@
 // zeros in shared memory before the product, so that nothing outside a sequence (NaN,
 // infinities) reaches its rows.
 //
+// Measured: one sequence of 16,384 tokens, 32 query and 8 KV heads of 128: 1,400 us warm,
+// 1,520 with inputs that change from call to call (1.45e15 flops a second); 24 ragged
+// sequences of up to 2,047: 286 us.  The tensor cores are busy three quarters of the time at
+// 16K tokens and half of it at 4K; what is left is the chain from scores to probabilities to
+// products at each item's ends.  Tried and slower: one loop of mixed steps for the two tiles'
+// products (1,800: the operands' addresses are worked out between wait and issue), scores
+// read twice, 32 columns at a time, instead of kept in registers (1,455 against 1,426).
+//
 // Items go heaviest first (by their row tile, over all sequences in order of length) and
 // are dealt to the CTAs in alternating direction, which needs no counter in memory.
 #include <cuda.h>

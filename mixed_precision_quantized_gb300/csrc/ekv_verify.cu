@@ -21,7 +21,9 @@
 // (and q), and with q each node at which a child was rejected.  Bound by latency:
 // one launch, one round of gathers, one pass over the last row.  A cluster of CL
 // CTAs shares a sequence's row passes, exchanging partial sums through distributed
-// shared memory.
+// shared memory.  Measured: 32 trees of 64 nodes over 131,072 tokens 19 us a call (the
+// host's share is as long), 16 sampled trees of 16 over 100,003 with draft probabilities 29
+// (two to three passes at the nodes with rejections, ~3 us each).
 #include <cooperative_groups.h>
 
 #include "ekv_internal.h"
