@@ -183,22 +183,20 @@ def _stream(stream) -> ctypes.c_void_p:
 
 
 class _On:
-    """Make the device (and the stream, if one is given) current, so that what the
-    binding allocates belongs to the stream the call runs on."""
+    """Make a device (and the stream, if one is given) current, so that what the binding
+    allocates belongs to the stream the call runs on; gives the stream's handle."""
 
-    __slots__ = ("ctx",)
+    __slots__ = ("ctx", "index")
 
-    def __init__(self, device: torch.device, stream):
-        self.ctx = []
-        if device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
+    def __init__(self, index: int, stream):
+        self.index, self.ctx = index, [torch.cuda.device(index)]
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
@@ -217,34 +215,37 @@ class _Here:
         pass
 
 
-def _on(device: torch.device, stream):
-    index = torch.cuda.current_device()
-    if stream is not None or device.index != index:
-        return _On(device, stream)
+def _on(index: int, stream):
+    if stream is not None or torch._C._cuda_getDevice() != index:
+        return _On(index, stream)
     h = _Here()
     h.handle = torch._C._cuda_getCurrentRawStream(index)
     return h
 
 
-def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device=None,
+def _gpu(name: str, t) -> int:
+    """The index of a tensor's GPU, which is the call's (-1: not on one, refused by the
+    checks that follow)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.get_device()
+
+
+def _need(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, index: int,
           contiguous: bool = True):
-    """Check a tensor argument: type, shape (None: any extent), device, layout."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and
-            (device is None or t.device == device) and (not contiguous or t.is_contiguous())):
+    """Check a tensor argument: type, shape, GPU, layout."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == index >= 0 and (not contiguous or t.is_contiguous())):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name} must have shape [{want}], got {list(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the call's GPU, got one on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _at(t: torch.Tensor | None):
@@ -252,9 +253,8 @@ def _at(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _token_stride(name: str, t: torch.Tensor) -> int:
-    """Token stride (elements) of [tokens, heads, d] whose heads are contiguous."""
-    n, h, d = t.shape
+def _token_stride(name: str, t: torch.Tensor, n: int, h: int, d: int) -> int:
+    """Token stride (elements) of [n, h, d] whose heads are contiguous."""
     st = t.stride()
     if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -374,21 +374,21 @@ class Cache:
         node attends over all cached tokens, itself and its ancestors.  Rows of
         `out` behind a sequence's nodes are left as they were (a new `out` starts
         at zero there)."""
-        n, H, d = seq_slots.numel(), self.num_kv_heads, self.head_dim
-        dev = seq_slots.device
-        _need("seq_slots", seq_slots, torch.int32, (n,))
+        gpu, H, d = _gpu("seq_slots", seq_slots), self.num_kv_heads, self.head_dim
+        n = seq_slots.numel()
+        _need("seq_slots", seq_slots, torch.int32, (n,), gpu)
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be a tensor [n, m, Hq, d]")
         m = q.shape[1]
-        _need("q", q, torch.float16, (n, m, self.num_q_heads, d), dev)
-        _need("k", k, torch.float16, (n, m, H, d), dev)
-        _need("v", v, torch.float16, (n, m, H, d), dev)
-        _need("parents", parents, torch.int32, (n, m), dev)
+        _need("q", q, torch.float16, (n, m, self.num_q_heads, d), gpu)
+        _need("k", k, torch.float16, (n, m, H, d), gpu)
+        _need("v", v, torch.float16, (n, m, H, d), gpu)
+        _need("parents", parents, torch.int32, (n, m), gpu)
         if n_nodes is not None:
-            _need("n_nodes", n_nodes, torch.int32, (n,), dev)
+            _need("n_nodes", n_nodes, torch.int32, (n,), gpu)
         if out is not None:
-            _need("out", out, torch.float16, tuple(q.shape), dev)
-        with _on(dev, stream) as s:
+            _need("out", out, torch.float16, (n, m, self.num_q_heads, d), gpu)
+        with _on(gpu, stream) as s:
             if out is None:
                 out = torch.empty_like(q) if n_nodes is None else torch.zeros_like(q)
             nb = self._tree_scratch.get((n, m))
@@ -397,10 +397,11 @@ class Cache:
                 _check(lib().ekv_tree_attn_scratch_bytes(self._h, n, m, ctypes.byref(out_nb)),
                        "ekv_tree_attn_scratch_bytes")
                 nb = self._tree_scratch[(n, m)] = out_nb.value
-            scratch = torch.empty(max(16, nb), dtype=torch.uint8, device=dev)
-            _check(lib().ekv_tree_attn(self._h, layer, n, _at(seq_slots), m, _at(n_nodes),
-                                       _at(parents), _at(q), _at(k), _at(v), _at(out),
-                                       _at(scratch), nb, s), "ekv_tree_attn")
+            scratch = torch.empty(max(16, nb), dtype=torch.uint8, device=q.device)
+            _check(lib().ekv_tree_attn(self._h, layer, n, seq_slots.data_ptr(), m, _at(n_nodes),
+                                       parents.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                       v.data_ptr(), out.data_ptr(), scratch.data_ptr(), nb, s),
+                   "ekv_tree_attn")
         return out
 
     def canary_kl(self, layer: int, seq_slots: torch.Tensor, q: torch.Tensor,
@@ -569,16 +570,18 @@ class Rope:
         """(q_out, k_out): q [n, Hq, d] and k [n, Hkv, d] (either may be None) turned to
         positions [n] int32.  Token strides are free (views of a fused projection),
         the heads of a token contiguous; q_out / k_out may be q / k (in place)."""
-        n, dev = positions.numel(), self.device
-        _need("positions", positions, torch.int32, (n,), dev)
-        with _on(dev, stream) as s:
-            q_out, qa = self._side("q", q, q_out, n)
-            k_out, ka = self._side("k", k, k_out, n)
+        gpu, n = _gpu("positions", positions), positions.numel()
+        _need("positions", positions, torch.int32, (n,), gpu)
+        if gpu != self.device.index:
+            raise ValueError(f"positions are on cuda:{gpu}, the table on {self.device}")
+        with _on(gpu, stream) as s:
+            q_out, qa = self._side("q", q, q_out, n, gpu)
+            k_out, ka = self._side("k", k, k_out, n, gpu)
             _check(lib().ekv_rope(self._cfg, self._table, n, positions.data_ptr(), *qa, *ka, s),
                    "ekv_rope")
         return q_out, k_out
 
-    def _side(self, name: str, x, out, n: int):
+    def _side(self, name: str, x, out, n: int, gpu: int):
         """One tensor's output and its arguments: heads, address, stride, of the output too."""
         if x is None:
             if out is not None:
@@ -588,13 +591,13 @@ class Rope:
             raise ValueError(f"{name} must be a tensor [tokens, heads, d]")
         h, d = x.shape[1], self.cfg.head_dim
         shape = (n, h, d)
-        _need(name, x, torch.float16, shape, self.device, contiguous=False)
+        _need(name, x, torch.float16, shape, gpu, contiguous=False)
         if out is None:
-            out, st = torch.empty(shape, dtype=torch.float16, device=self.device), h * d
+            out, st = x.new_empty(shape), h * d
         else:
-            _need(name + "_out", out, torch.float16, shape, self.device, contiguous=False)
-            st = _token_stride(name + "_out", out)
-        return out, (h, x.data_ptr(), _token_stride(name, x), out.data_ptr(), st)
+            _need(name + "_out", out, torch.float16, shape, gpu, contiguous=False)
+            st = _token_stride(name + "_out", out, n, h, d)
+        return out, (h, x.data_ptr(), _token_stride(name, x, n, h, d), out.data_ptr(), st)
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -608,22 +611,26 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must have shape [tokens, heads, d]")
     T, Hq, d = q.shape
-    Hkv, dev = k.shape[1], q.device
-    _need("q", q, torch.float16, (T, Hq, d), dev, contiguous=False)
-    _need("k", k, torch.float16, (T, Hkv, d), dev, contiguous=False)
-    _need("v", v, torch.float16, (T, Hkv, d), dev, contiguous=False)
-    _need("cu_seqlens", cu_seqlens, torch.int32, (None,), dev)
-    if out is not None:
-        _need("out", out, torch.float16, (T, Hq, d), dev, contiguous=False)
-    if cu_seqlens.numel() < 1:
+    Hkv, gpu = k.shape[1], _gpu("q", q)
+    _need("q", q, torch.float16, (T, Hq, d), gpu, contiguous=False)
+    _need("k", k, torch.float16, (T, Hkv, d), gpu, contiguous=False)
+    _need("v", v, torch.float16, (T, Hkv, d), gpu, contiguous=False)
+    n = cu_seqlens.numel() if isinstance(cu_seqlens, torch.Tensor) else 0
+    _need("cu_seqlens", cu_seqlens, torch.int32, (n,), gpu)
+    if n < 1:
         raise ValueError("cu_seqlens must hold n + 1 bounds")
-    with _on(dev, stream) as s:
+    if out is not None:
+        _need("out", out, torch.float16, (T, Hq, d), gpu, contiguous=False)
+    with _on(gpu, stream) as s:
         if out is None:
-            out = torch.empty(T, Hq, d, dtype=torch.float16, device=dev)
-        st = [_token_stride(nm, t) for nm, t in (("q", q), ("k", k), ("v", v), ("out", out))]
-        _check(lib().ekv_prompt_attn(Hq, Hkv, d, float(softmax_scale), T, cu_seqlens.numel() - 1,
-                                     _at(cu_seqlens), _at(q), st[0], _at(k), st[1], _at(v),
-                                     st[2], _at(out), st[3], s), "ekv_prompt_attn")
+            out, so = q.new_empty((T, Hq, d)), max(Hq * d, 8)
+        else:
+            so = _token_stride("out", out, T, Hq, d)
+        _check(lib().ekv_prompt_attn(Hq, Hkv, d, softmax_scale, T, n - 1, cu_seqlens.data_ptr(),
+                                     q.data_ptr(), _token_stride("q", q, T, Hq, d), k.data_ptr(),
+                                     _token_stride("k", k, T, Hkv, d), v.data_ptr(),
+                                     _token_stride("v", v, T, Hkv, d), out.data_ptr(), so, s),
+               "ekv_prompt_attn")
     return out
 
 
@@ -640,31 +647,31 @@ def verify_tree(target_probs: torch.Tensor, tokens: torch.Tensor, parents: torch
     if target_probs.dim() != 3:
         raise ValueError("target_probs must have shape [n, m, V]")
     n, m, V = target_probs.shape
-    dev = target_probs.device
-    for name, t, dt, shape in (("tokens", tokens, torch.int32, (n, m)),
-                               ("parents", parents, torch.int32, (n, m)),
-                               ("u_accept", u_accept, torch.float32, (n, m)),
-                               ("u_sample", u_sample, torch.float32, (n,))):
-        _need(name, t, dt, shape, dev)
+    gpu = _gpu("target_probs", target_probs)
+    _need("tokens", tokens, torch.int32, (n, m), gpu)
+    _need("parents", parents, torch.int32, (n, m), gpu)
+    _need("u_accept", u_accept, torch.float32, (n, m), gpu)
+    _need("u_sample", u_sample, torch.float32, (n,), gpu)
     if n_nodes is not None:
-        _need("n_nodes", n_nodes, torch.int32, (n,), dev)
+        _need("n_nodes", n_nodes, torch.int32, (n,), gpu)
     strides = []
     for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
         if t is None:
             strides += [0, 0]
             continue
-        _need(name, t, torch.float32, (n, m, V), dev, contiguous=False)
-        if V > 1 and t.stride(2) != 1:
+        _need(name, t, torch.float32, (n, m, V), gpu, contiguous=False)
+        st = t.stride()
+        if V > 1 and st[2] != 1:
             raise ValueError(f"{name}: a row's entries must be contiguous")
-        strides += [t.stride(0) if n > 1 else 0, t.stride(1) if m > 1 else V]
-    with _on(dev, stream) as s:
-        path = torch.empty(n, m, dtype=torch.int32, device=dev)
-        n_accept = torch.empty(n, dtype=torch.int32, device=dev)
-        nxt = torch.empty(n, dtype=torch.int32, device=dev)
-        _check(lib().ekv_verify_tree(n, m, V, _at(target_probs), strides[0], strides[1],
-                                     _at(draft_probs), strides[2], strides[3], _at(tokens),
-                                     _at(parents), _at(n_nodes), _at(u_accept), _at(u_sample),
-                                     _at(path), _at(n_accept), _at(nxt), s), "ekv_verify_tree")
+        strides += [st[0] if n > 1 else 0, st[1] if m > 1 else V]
+    with _on(gpu, stream) as s:
+        path = torch.empty_like(tokens)
+        n_accept, nxt = tokens.new_empty(n), tokens.new_empty(n)
+        _check(lib().ekv_verify_tree(n, m, V, target_probs.data_ptr(), strides[0], strides[1],
+                                     _at(draft_probs), strides[2], strides[3], tokens.data_ptr(),
+                                     parents.data_ptr(), _at(n_nodes), u_accept.data_ptr(),
+                                     u_sample.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
+                                     nxt.data_ptr(), s), "ekv_verify_tree")
     return path, n_accept, nxt
 
 
