@@ -128,8 +128,8 @@ struct TMisc {
   int32_t has_lo[KST];
   alignas(16) int32_t ent[RAW_MAX][TPAGES];  // page-table entries of a raw tile
   int32_t raw_lo[RAW_MAX];                   // whether its K needs the lo products
-  float mx[2][TM_ROWS];         // row maxima of the two groups, then their (sum, z)
-  float lz[2][2][TM_ROWS];
+  float mx[2][TM_ROWS];         // row maxima of the two groups
+  float lz[2][2][TM_ROWS];      // their row sums and zero-point sums
   alignas(8) uint64_t bars[2 * KST + 3 * VST + 2 * RAW_MAX + 1 + 4 + 4 + 2];
   Runs runs;
   Walk walk[TT / 32];

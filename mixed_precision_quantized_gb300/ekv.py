@@ -303,6 +303,7 @@ class Cache:
         vb = (ctypes.c_uint8 * num_layers)(*self.v_bits)
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
+            self._gpu = torch.cuda.current_device()
             _check(L.ekv_create(ctypes.byref(cfg), kb, vb, ctypes.byref(h)), "ekv_create")
         self._h = h
 
@@ -374,8 +375,9 @@ class Cache:
         node attends over all cached tokens, itself and its ancestors.  Rows of
         `out` behind a sequence's nodes are left as they were (a new `out` starts
         at zero there)."""
-        gpu, H, d = _gpu("seq_slots", seq_slots), self.num_kv_heads, self.head_dim
-        n = seq_slots.numel()
+        if not isinstance(seq_slots, torch.Tensor):
+            raise TypeError("seq_slots must be a tensor")
+        gpu, H, d, n = self._gpu, self.num_kv_heads, self.head_dim, seq_slots.numel()
         _need("seq_slots", seq_slots, torch.int32, (n,), gpu)
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be a tensor [n, m, Hq, d]")
