@@ -21,7 +21,8 @@
 // (and q), and with q each node at which a child was rejected.  Bound by latency:
 // one launch, one round of gathers, one pass over the last row.  A cluster of CL
 // CTAs shares a sequence's row passes, exchanging partial sums through distributed
-// shared memory.  Measured: 32 trees of 64 nodes over 131,072 tokens 19 us a call (the
+// shared memory (no CTA writes another's before a cluster barrier has shown that it runs,
+// and none leaves while another may write its own).  Measured: 32 trees of 64 nodes over 131,072 tokens 19 us a call (the
 // host's share is as long), 16 sampled trees of 16 over 100,003 with draft probabilities 29
 // (two to three passes at the nodes with rejections, ~3 us each).
 #include <cooperative_groups.h>
@@ -115,6 +116,8 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
   __shared__ uint64_t s_wsum[VWARPS], s_part[2][CL], s_z[VMAX];
   const int z = blockIdx.x / CL, rank = blockIdx.x % CL;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Waited for before the walk: the gathers lie between.
+  if constexpr (CL > 1) cg::this_cluster().barrier_arrive();
   const int V = A.vocab;
   const int cnt = A.n_nodes ? min(A.m, A.n_nodes[z]) : A.m;
   const float* P = A.p + z * A.p_seq;
@@ -235,6 +238,7 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
     return total;
   };
 
+  if constexpr (CL > 1) cg::this_cluster().barrier_wait();
   // The walk, the same in every thread of the cluster.
   int node = 0, nacc = 0, k = 0, ngone = 0;
   uint64_t total = 0;

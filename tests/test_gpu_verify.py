@@ -65,6 +65,23 @@ def test_walks(n, m, V, shape, draft):
 
 
 @pytest.mark.parametrize("draft", [False, True], ids=["target", "draft"])
+@pytest.mark.parametrize("V", [8192, 8193, 9001])
+def test_rows_shared_by_a_cluster(V, draft):
+    """Rows just past the size from which CTAs of a cluster share them (some have an empty
+    slice and reach the exchange of sums first), more sequences than run at once, trees
+    of no nodes among them; three calls in a row give the same."""
+    n = 400
+    p, q, tok, par, u, us = _case(V, 8, 5, V, draft)
+    pick = np.random.default_rng(V).integers(0, 8, n)
+    c = [None if x is None else x[pick] for x in (p, q, tok, par)]
+    u = np.random.default_rng(V + 1).random((n, 5)).astype(np.float32)
+    us = np.random.default_rng(V + 2).random(n).astype(np.float32)
+    cnt = np.random.default_rng(V + 3).integers(0, 6, n).astype(np.int32)
+    for _ in range(3):
+        _check(*c, u, us, cnt=cnt)
+
+
+@pytest.mark.parametrize("draft", [False, True], ids=["target", "draft"])
 @pytest.mark.parametrize("seed", range(6))
 def test_many_small_trees(seed, draft):
     """200 trees of up to 24 nodes over 50 tokens: every outcome occurs."""
