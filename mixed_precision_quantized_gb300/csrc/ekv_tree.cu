@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int tok = lane + 32 * u, pg = tok / BLOCK, r = tok % BLOCK;
-            float s = 1.f, zv = 0.f;  // (rows of scale 0 hold zero codes only: any scale does)
+            float s = 1.f, zv = 0.f;
             bool there = tok < n;
             if (!drafts) {
               const int32_t e = M.ent[rs][pg];
@@ -798,10 +798,15 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
                 else  // the open block
                   sp = reinterpret_cast<const __half*>(
                       st.pool_base[fmt] + off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt]);
+                // A row of scale 0 holds zero codes (symmetric: signed 0, so any scale does;
+                // asymmetric: unsigned 0, -2^(b-1) once centred, which the zero point below
+                // cancels at any scale).  The smallest fp16 leaves the least of a rounded
+                // probability times that code, and does not raise the reference above the
+                // other rows' scaled values.
                 s = __half2float(sp[r]);
+                if (s == 0.f) s = 0x1p-24f;
                 if (ASYM)
                   zv = fmaf(s, (float)(1 << (A.vb - 1)), __half2float(sp[BLOCK + r]));
-                if (s == 0.f) s = 1.f;
               }
             }
             const float inv = __fdividef(1.f, s), y = __log2f(s) * A.k_ext;

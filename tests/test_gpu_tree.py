@@ -86,6 +86,21 @@ class Case:
         w = span * 2.0 ** (self.vb - 1) / (2.0 ** self.vb - 2)
         return np.concatenate([w, np.zeros((c, self.hkv, 1))])
 
+    def refill(self, k, v, kb):
+        """The first sequence holds the rows k, v [T, Hkv, d] instead, K at kb bits."""
+        self.cache.reset(self.order[0])
+        self.cache.set_tiers([kb])
+        self.state[0], self.lens[0] = SeqState(self.hkv, self.d, self.vb, None, None, self.asym), len(k)
+        self.cache.append(0, self.slots[:1], torch.from_numpy(k[None]).cuda(),
+                          torch.from_numpy(v[None]).cuda())
+        self.state[0].append(k, v, kb)
+
+    def attend(self, q, k, v, par):
+        o = self.cache.tree_attn(0, self.slots, q, k, v, torch.from_numpy(par).cuda())
+        self.cache.sync()
+        self.check(o, q, k, v, par)
+        return o
+
     def run(self, m, shape="tree", cnt=None, q_scale=1.0):
         q, k, v, par = self.drafts(m, shape, q_scale)
         out = torch.full_like(q, 9.0)
@@ -193,6 +208,50 @@ def test_zero_values_beside_large_logits(case):
     o = c.cache.tree_attn(0, c.slots, q, kd, vd, torch.from_numpy(par).cuda())
     c.cache.sync()
     c.check(o, q, kd, vd, par)
+
+
+@pytest.mark.parametrize("asym", [False, True], ids=["sym", "asym"])
+@pytest.mark.parametrize("vb", [2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("row", ["zero", "constant", "small span"])
+@pytest.mark.parametrize("boost", [0.0, 60.0])
+def test_value_rows_of_scale_zero(case, asym, vb, d, row, boost):
+    """Value rows whose stored scale is 0 (all zero; equal entries and a span below the
+    smallest scale, with the asymmetric quantizer), in sealed blocks and the open one,
+    with logits as the others' and far above them.  What such a row adds is its zero
+    point; a rounded probability (2^-11) times the centred code 2^(vb-1) <= 2^7 at the
+    smallest fp16 scale 2^-24 is below 2^-28, inside the bound's 2^-24."""
+    c = case([64], 4, 2, d, [16], vb, asym)
+    T = 55
+    k, v = (c.rng.normal(size=(T, 2, d)).astype(np.float16) for _ in range(2))
+    at = [2, 17, 40, 50]
+    v[at] = 3.5 if row == "constant" else 0.0
+    if row == "small span":
+        v[at, :, ::3] = 2.0 ** -24
+    k[at, :, 0] = boost
+    c.refill(k, v, 16)
+    q, kd, vd, par = c.drafts(3)
+    q[..., 0] = 1.0
+    c.attend(q, kd, vd, par)
+
+
+@pytest.mark.parametrize("vb", [2, 4, 8])
+@pytest.mark.parametrize("nats", [0.0, 4.0, 8.0, 12.0])
+def test_small_values_beside_zero_rows(case, vb, nats):
+    """Zero rows whose logits lead by `nats` over rows of values near 1e-4: the others'
+    probabilities keep their bits (the reference follows the scaled values)."""
+    T = 3000
+    c = case([T], 2, 2, 64, [16], vb)
+    k = c.rng.normal(size=(T, 2, 64)).astype(np.float16)
+    v = (1e-4 * c.rng.normal(size=(T, 2, 64))).astype(np.float16)
+    v[100:104] = 0
+    k[:, :, 0] = 0
+    k[100:104, :, 0] = nats
+    c.refill(k, v, 16)
+    q, kd, vd, par = c.drafts(3)
+    q[..., 0] = 8.0
+    kd[..., 0] = -100.0  # leaves the drafts' own values out
+    c.attend(q, kd, vd, par)
 
 
 def test_more_sequences_than_one_launch_takes(case):
