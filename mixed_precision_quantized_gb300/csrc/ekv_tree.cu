@@ -15,7 +15,8 @@
 //   warps 8-15   unpack a raw tile into swizzled fp16 operand tiles, a page's K or V a warp
 //                (K on schedulers 0 and 1, V on 2 and 3: less code for each): K as hi + lo
 //                (khat = code * scale = hi + lo exactly, two products; 2- and 16-bit K need
-//                hi alone), V as the bare codes (exact in fp16)
+//                hi alone; asymmetric: hi + lo = code * scale + zero point to 22 bits), V as
+//                the bare codes (exact in fp16)
 //   warp 18      the V scales of a tile, for softmax
 //   warps 16, 19 tcgen05.mma: S = Q K^T with Q in tensor memory, and O += P V (a warp each:
 //                their waits in one loop took longer than the products)
@@ -264,6 +265,16 @@ __device__ __forceinline__ uint32_t hfms(uint32_t a, uint32_t b, uint32_t c) {  
                             __hneg2(*reinterpret_cast<__half2*>(&c)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t hmin(uint32_t a, uint32_t b) {
+  const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// (a, b) as fp16, the largest finite value instead of infinity.
+__device__ __forceinline__ uint32_t pack_finite(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
 __device__ __forceinline__ void perm8(const uint4& u, uint32_t* w) {
   w[0] = __byte_perm(u.x, u.z, 0x5410);
   w[1] = __byte_perm(u.x, u.z, 0x7632);
@@ -369,9 +380,15 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
   constexpr int STEP = Lane<D>::STEP;
   constexpr int R = KB < 8 && !ASYM ? 4 : 2;  // rows at once
   constexpr bool HAS_LO = KB < 16 && (ASYM || KB > 2);
-  uint32_t sc[4], zp[4];
+  // A scale rounds up in fp16, so the largest code times it may pass fp16's range (127 * 516,
+  // 7 * 9360 for entries of 65504).  hi is formed with the scale cut to where it cannot
+  // (515.5, 9352); lo = code * scale - hi stays exact: a small multiple of the scale's step.
+  constexpr uint32_t TOP = both(KB == 8 ? 0x6007 : 0x7091);
+  uint32_t sc[4], top[4], zp[4];
   if constexpr (KB < 16) {
     channel8<KB>(kp + BLOCK * D * KB / 8, ln.g, sc);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) top[x] = KB > 2 && !ASYM ? hmin(sc[x], TOP) : sc[x];
     if constexpr (ASYM) channel8<KB>(kp + BLOCK * D * KB / 8 + 2 * D, ln.g, zp);
   }
 #pragma unroll 1
@@ -393,7 +410,7 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
         if constexpr (KB < 16 && !ASYM) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint32_t p = hmul(w[x], sc[x]);
+            const uint32_t p = hmul(w[x], top[x]);
             if constexpr (KB > 2) l[x] = hfms(w[x], sc[x], p);  // the exact residual
             w[x] = p;
           }
@@ -404,10 +421,9 @@ __device__ __forceinline__ void unpack_k(const uint8_t* kp, int64_t stride, int 
             const float2 s = __half22float2(*reinterpret_cast<__half2*>(&sc[x]));
             const float2 z = __half22float2(*reinterpret_cast<__half2*>(&zp[x]));
             const float a = fmaf(u.x, s.x, z.x), b = fmaf(u.y, s.y, z.y);
-            const __half2 p = __floats2half2_rn(a, b);
-            const float2 pf = __half22float2(p);
+            w[x] = pack_finite(a, b);  // (u s + z may pass fp16's range as well)
+            const float2 pf = __half22float2(*reinterpret_cast<__half2*>(&w[x]));
             const __half2 r = __floats2half2_rn(a - pf.x, b - pf.y);
-            w[x] = *reinterpret_cast<const uint32_t*>(&p);
             l[x] = *reinterpret_cast<const uint32_t*>(&r);
           }
         }

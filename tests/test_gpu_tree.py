@@ -254,6 +254,33 @@ def test_small_values_beside_zero_rows(case, vb, nats):
     c.attend(q, kd, vd, par)
 
 
+@pytest.mark.parametrize("asym", [False, True], ids=["sym", "asym"])
+@pytest.mark.parametrize("kb", [2, 4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_largest_keys(case, asym, kb, d):
+    """Key channels at fp16's end (what a saturated projection holds): their scales round
+    up, so the largest stored values lie past 65504.  Such channels have small queries
+    (2^-13), so that the other channels count too; decode attention on the same cache
+    agrees (the tree's one node points away from every query)."""
+    c = case([64], 4, 2, d, [kb], 16, asym)
+    T = 53
+    k, v = (c.rng.normal(size=(T, 2, d)).astype(np.float16) for _ in range(2))
+    k[:, 0, 3] = np.where(np.arange(T) % 2, 65504, -65504)
+    k[:, 1, 5] = 65504 - 32 * (np.arange(T) % 5)
+    k[:16, 1, 7] = -65504
+    k[3, 1, 7] = 60000
+    c.refill(k, v, kb)
+    q, kd, vd, par = c.drafts(3)
+    q[..., [3, 5, 7]] *= 2.0 ** -13
+    c.attend(q, kd, vd, par)
+    q[:, :, 1], q[:, :, 3] = q[:, :, 0], q[:, :, 2]
+    kd = -8 * q[:, :, ::2]
+    o = c.attend(q[:, :1].contiguous(), kd[:, :1].contiguous(), vd[:, :1].contiguous(), par[:, :1])
+    b = c.cache.decode_attn(0, c.slots, q[:, 0].contiguous()).float()
+    c.cache.sync()
+    assert torch.all((o[:, 0].float() - b).abs() <= 2e-3 + 1e-2 * b.abs())
+
+
 def test_more_sequences_than_one_launch_takes(case):
     """300 sequences of 0 to 40 tokens (a launch takes 256)."""
     lens = np.random.default_rng(2).integers(0, 41, 300).tolist()
