@@ -26,11 +26,11 @@ class Case:
     run of tokens each), and its oracle."""
 
     def __init__(self, lens, hq, hkv, d, kbits, vb, asym=False, seed=0, gain=8.0, slots=None,
-                 max_seqs=None, v_scale=1.0):
+                 max_seqs=None, v_scale=1.0, room=16):
         self.lens, self.hq, self.hkv, self.d, self.vb, self.asym = lens, hq, hkv, d, vb, asym
         self.rng = np.random.default_rng(seed)
-        pages = sum(-(-t // 16) + len(kbits) for t in lens) * hkv + 1
-        self.cache = ekv.Cache(1, max_seqs or len(lens), hq, hkv, d, max(max(lens), 16),
+        pages = sum(-(-max(t, room) // 16) + len(kbits) for t in lens) * hkv + 1
+        self.cache = ekv.Cache(1, max_seqs or len(lens), hq, hkv, d, max(max(lens), room),
                                {(b, vb): pages for b in set(kbits)}, [kbits[0]], [vb], asym=asym)
         self.order = list(range(len(lens))) if slots is None else slots
         self.slots = torch.tensor(self.order, dtype=torch.int32, device="cuda")
@@ -86,14 +86,14 @@ class Case:
         w = span * 2.0 ** (self.vb - 1) / (2.0 ** self.vb - 2)
         return np.concatenate([w, np.zeros((c, self.hkv, 1))])
 
-    def refill(self, k, v, kb):
-        """The first sequence holds the rows k, v [T, Hkv, d] instead, K at kb bits."""
-        self.cache.reset(self.order[0])
+    def refill(self, k, v, kb, z=0):
+        """Sequence z holds the rows k, v [T, Hkv, d] instead, K at kb bits."""
+        self.cache.reset(self.order[z])
         self.cache.set_tiers([kb])
-        self.state[0], self.lens[0] = SeqState(self.hkv, self.d, self.vb, None, None, self.asym), len(k)
-        self.cache.append(0, self.slots[:1], torch.from_numpy(k[None]).cuda(),
+        self.state[z], self.lens[z] = SeqState(self.hkv, self.d, self.vb, None, None, self.asym), len(k)
+        self.cache.append(0, self.slots[z:z + 1], torch.from_numpy(k[None]).cuda(),
                           torch.from_numpy(v[None]).cuda())
-        self.state[0].append(k, v, kb)
+        self.state[z].append(k, v, kb)
 
     def attend(self, q, k, v, par):
         o = self.cache.tree_attn(0, self.slots, q, k, v, torch.from_numpy(par).cuda())
@@ -235,22 +235,31 @@ def test_value_rows_of_scale_zero(case, asym, vb, d, row, boost):
     c.attend(q, kd, vd, par)
 
 
-@pytest.mark.parametrize("vb", [2, 4, 8])
+@pytest.mark.parametrize("asym", [False, True], ids=["sym", "asym"])
+@pytest.mark.parametrize("vb", [2, 4, 8, 16])
+@pytest.mark.parametrize("size", [0.1, 1e-2, 1e-3, 1e-4])
 @pytest.mark.parametrize("nats", [0.0, 4.0, 8.0, 12.0])
-def test_small_values_beside_zero_rows(case, vb, nats):
-    """Zero rows whose logits lead by `nats` over rows of values near 1e-4: the others'
-    probabilities keep their bits (the reference follows the scaled values)."""
-    T = 3000
-    c = case([T], 2, 2, 64, [16], vb)
-    k = c.rng.normal(size=(T, 2, 64)).astype(np.float16)
-    v = (1e-4 * c.rng.normal(size=(T, 2, 64))).astype(np.float16)
-    v[100:104] = 0
-    k[:, :, 0] = 0
-    k[100:104, :, 0] = nats
-    c.refill(k, v, 16)
+@pytest.mark.parametrize("lead", ["drafts", "zero rows"])
+def test_small_values_beside_rows_that_lead(case, asym, vb, size, nats, lead):
+    """Values of one sign near `size` under equal logits, and drafts or zero rows whose
+    logits lead by `nats`: each cached probability is small, rounds alike, and all of them
+    together count.  They keep their bits, because the reference follows the probabilities
+    times the values' scales, the drafts' among them.  (64 tokens a sequence and more units
+    than CTAs: the cached tile and the drafts' share a reference.)"""
+    n, T, h, d = (48, 64, 4, 64) if lead == "drafts" else (1, 2000, 2, 64)
+    c = case([0] * n, h, h, d, [16], vb, asym, room=T)
+    for z in range(n):
+        k = np.zeros((T, h, d), np.float16)
+        v = (size * (1 + 0.1 * c.rng.normal(size=(T, h, d)))).astype(np.float16)
+        if lead == "zero rows":
+            v[100:104] = 0
+            k[100:104, :, 0] = nats
+        c.refill(k, v, 16, z)
     q, kd, vd, par = c.drafts(3)
     q[..., 0] = 8.0
-    kd[..., 0] = -100.0  # leaves the drafts' own values out
+    vd = (size * vd.float()).half()
+    kd[:] = 0
+    kd[..., 0] = nats if lead == "drafts" else -100.0
     c.attend(q, kd, vd, par)
 
 
@@ -279,6 +288,23 @@ def test_largest_keys(case, asym, kb, d):
     b = c.cache.decode_attn(0, c.slots, q[:, 0].contiguous()).float()
     c.cache.sync()
     assert torch.all((o[:, 0].float() - b).abs() <= 2e-3 + 1e-2 * b.abs())
+
+
+@pytest.mark.parametrize("asym", [False, True], ids=["sym", "asym"])
+@pytest.mark.parametrize("vb", [2, 4, 8, 16])
+@pytest.mark.parametrize("d,m", [(64, 16), (128, 33), (64, 64)])
+def test_draft_values_of_every_size(case, asym, vb, d, m):
+    """Drafted value rows from zero and the smallest fp16 to the largest, one size a node
+    (each node's own logit leads, so that its row shows), over cached values of 1 and of
+    none: sequences without cached tokens too."""
+    c = case([100, 0], 4, 2, d, [4], vb, asym)
+    q, kd, vd, par = c.drafts(m)
+    size = torch.logspace(-24, 15, m, base=2.0, device="cuda").view(1, m, 1, 1)
+    size[0, m // 2] = 0
+    vd = (size * vd.float().clamp(-1.9, 1.9)).half()
+    q[:, :, 1], q[:, :, 3] = q[:, :, 0], q[:, :, 2]
+    kd = (0.7 * q[:, :, ::2].float()).half()
+    c.attend(q, kd, vd, par)
 
 
 def test_more_sequences_than_one_launch_takes(case):
