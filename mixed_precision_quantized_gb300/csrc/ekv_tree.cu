@@ -38,9 +38,11 @@
 // softmax thread from shared memory (140), polling waits without a suspend hint (203).
 //
 // A token's V scale s multiplies its probability: P' = 2^(x + log2 s - m) in fp16, where
-// the reference m follows the largest x + log2 s, so the fp16 range goes to what the tokens
-// add to the output, whatever the scales (the drafts' raw rows get one of their own beside
-// quantized pages; with 16-bit V every scale is 1); the row sum adds P' / s in fp32.  The log2 s come with the scores: 16 more
+// the reference m follows the largest x + log2 s, so the fp16 range goes to what the cached
+// tokens add to the output, whatever their scales; the row sum adds P' / s in fp32.  The
+// drafts' raw rows have s = 1, which may be far above the others': their tile, the last, is
+// alone in its pair, so a reference that they raise rescales the accumulator in fp32 and
+// takes no bits from any cached token's P'.  The log2 s come with the scores: 16 more
 // channels of K hold log2 s / (sigma log2 e) as three fp16 parts, against a constant in Q
 // (each softmax thread loading 64 of them twice from shared memory took longer than the
 // exponentials).  As in prompt attention m moves only for a gain above 2^8, P' carries
@@ -105,6 +107,9 @@ struct Seg {
   int z, h, row0, s, e, nt, len, cnt;
   int slot;  // of its partial
   __device__ bool whole() const { return s == 0 && e == nt; }
+  // Tiles left out at the start of the first pair (0 or 1), so that the drafts' tile is alone in
+  // its pair.
+  __device__ int skip() const { return e == nt && !((e - s) & 1); }
   // Tokens of page pg of tile i (its raw tile in slot rs).
   __device__ int tokens(int i, const TMisc& M, int rs, int pg) const;
 };
@@ -123,8 +128,7 @@ struct TMisc {
   int32_t slot[TSEQS];
   uint8_t cnt[TSEQS];           // nodes
   unsigned long long anc[2][64];  // ancestors-or-self of each node, by segment parity
-  // of each token's V scale s: 1 / s and (asymmetric) the zero point over s (a draft's s
-  // itself on its way from the unpacking warps to W_SCALES)
+  // of each token's V scale s: 1 / s and (asymmetric) the zero point over s
   alignas(16) float rsv[VST][TN];
   alignas(16) float zsv[VST][TN];
   alignas(8) uint16_t valid[VST][TPAGES];  // tokens that are there
@@ -466,41 +470,6 @@ __device__ __forceinline__ void unpack_v(const uint8_t* vp, int64_t stride, int 
   }
 }
 
-// The drafts' V rows beside quantized pages, where they need a scale as the cached rows have
-// one: each row times a power of two that brings its largest entry to [64, 128) if it is below
-// that (exact; at most 2^15), and `scale` (rows of this page) its inverse.  Rows from n on
-// become zero.
-template <int D>
-__device__ __forceinline__ void unpack_draft_v(const uint8_t* vp, int64_t stride, int n,
-                                               uint8_t* dst, float* scale, const Lane<D>& ln) {
-  constexpr int STEP = Lane<D>::STEP, GR = Lane<D>::GR;
-#pragma unroll 1
-  for (int c = 0; c < BLOCK; c += 4 * STEP) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = c + ln.t0 + j * STEP;
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (r < n) {
-        Raw8<16> raw;
-        raw.load(vp + r * stride, ln.g);
-        unpack8w<16, false>(raw, w);
-      }
-      // the exponent field of the row's largest magnitude (bit patterns order as magnitudes)
-      uint32_t m = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) m = max(m, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
-#pragma unroll
-      for (int off = 1; off < GR; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-      const int k = max(0, min(15, 21 - (int)(m >> 10)));
-      const uint32_t f = both((uint32_t)(15 + k) << 10);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) w[x] = hmul(w[x], f);
-      *reinterpret_cast<uint4*>(dst + c * 128 + ln.off[j]) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (ln.g == 0) scale[r] = __int_as_float((127 - k) << 23);
-    }
-  }
-}
-
 // The loop of an unpacking warp: one page of every tile, its K or its V part.
 template <int D, bool ASYM, bool IS_K>
 __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& A, uint8_t* smem,
@@ -570,10 +539,8 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
           }
         } else if (drafts) {
           const __half* vp = A.v + (((size_t)w.z * A.m + BLOCK * pg) * st.Hkv + w.h) * D;
-          const uint8_t* rows = reinterpret_cast<const uint8_t*>(vp);
-          const int64_t stride = 2 * D * (int64_t)st.Hkv;
-          if (A.vb == 16) unpack_v<D, 16, false>(rows, stride, n, dst, hf);
-          else unpack_draft_v<D>(rows, stride, n, dst, M.rsv[at] + pg * BLOCK, hf);
+          unpack_v<D, 16, false>(reinterpret_cast<const uint8_t*>(vp), 2 * D * (int64_t)st.Hkv, n,
+                                 dst, hf);
         } else {  // the open block, or no tokens (zeros)
           const uint8_t* vp =
               n > 0 ? st.pool_base[fmt] + v_off + (size_t)entry_idx(e) * st.pool_page_bytes[fmt]
@@ -750,14 +717,14 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       uint32_t kph = 0, qph = 0, oph = 3;  // a buffer's first scores wait for no product
       bool ok = true;
       while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
-        const int n = w.e - w.s;
+        const int x0 = w.skip(), n = x0 + w.e - w.s;
         ok = warp_wait(q_full, qph, stop);
         qph ^= 1;
 #pragma unroll 1
-        for (int x = 0; x < n && ok; ++x) {
+        for (int x = x0; x < n && ok; ++x) {
           const int t = x & 1;
           ok = warp_wait(k_full + 8 * sg, kph, stop);
-          if (t == 0) {  // the buffer's last probabilities have been used
+          if (t == 0 || x == x0) {  // the buffer's last probabilities have been used
             ok = ok && warp_wait(o_done + 8 * buf, (oph >> buf) & 1, stop);
             oph ^= 1u << buf;
           }
@@ -793,9 +760,9 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       uint32_t vph = 0, pph = 0;
       bool ok = true;
       while (ok && next_seg(&M.walk[warp], M, A, st, lane, w)) {
-        const int n = w.e - w.s;
+        const int x0 = w.skip(), n = x0 + w.e - w.s;
 #pragma unroll 1
-        for (int x = 0; x < n && ok; ++x) {
+        for (int x = x0; x < n && ok; ++x) {
           const int t = x & 1, i = 2 * buf + t;
           ok = warp_wait(v_full + 8 * sg, vph, stop) &&
                warp_wait(p_full + 8 * i, (pph >> i) & 1, stop);
@@ -804,7 +771,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           fence_after();
           const uint32_t base = uniform(sb + Cfg::V_OFF + sg * Cfg::OPND);
           const uint32_t p = uniform(tm + 256 + 128 * buf + 64 * t);
-          const bool acc = uniform(x > 0), last = uniform(t == 1 || x == n - 1);
+          const bool acc = uniform(x > x0), last = uniform(t == 1 || x == n - 1);
           if (elect()) {
 #pragma unroll
             for (int k = 0; k < TN / 16; ++k)
@@ -833,17 +800,13 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           ok = ok && warp_wait(k_empty + 8 * ks, kph, stop);
           ok = ok && warp_wait(v_empty + 8 * vs, eph, stop);
           if (!ok) break;
-          // (the drafts' scales come from the warps that unpack their V)
-          if (drafts && A.vb < 16 && !(ok = warp_wait(v_full + 8 * vs, eph ^ 1, stop))) break;
           const int n = drafts ? min(TN, w.cnt) : min(TN, w.len - i * TN);  // tokens of the tile
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int tok = lane + 32 * u, pg = tok / BLOCK, r = tok % BLOCK;
             float s = 1.f, zv = 0.f;
             bool there = tok < n;
-            if (drafts) {
-              if (there && A.vb < 16) s = M.rsv[vs][tok];
-            } else {
+            if (!drafts) {
               const int32_t e = M.ent[rs][pg];
               there = there && e != -1;
               if (there && A.vb < 16) {
@@ -973,12 +936,12 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       uint64_t l2 = pack2(0.f, 0.f), z2 = pack2(0.f, 0.f);
       const int n = w.e - w.s;
 #pragma unroll 1
-      for (int x0 = 0; x0 < n; x0 += 2) {
-        const bool have = x0 + t < n && !idle;
+      for (int x0 = -w.skip(); x0 < n; x0 += 2) {
+        const bool there = x0 + t >= 0 && x0 + t < n, have = there && !idle;
         const int at = tiles + x0 + t, sg = at % VST;  // V stages go round over all tiles
         const uint32_t ts = base + 256 + 128 * buf + 64 * t;
         const int bi = 2 * buf + t;
-        if (x0 + t < n) {
+        if (there) {
           ok = ok && warp_wait(sc_full + 8 * sg, (at / VST) & 1, stop);
           ok = ok && warp_wait(s_full + 8 * bi, (sph >> bi) & 1, stop);
           sph ^= 1u << bi;
@@ -1088,7 +1051,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           }
           tmem_wait_st();
         }
-        if (x0 + t < n) {
+        if (there) {
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(p_full + 8 * bi);

@@ -244,8 +244,8 @@ def test_small_values_beside_rows_that_lead(case, asym, vb, size, nats, lead):
     """Values of one sign near `size` under equal logits, and drafts or zero rows whose
     logits lead by `nats`: each cached probability is small, rounds alike, and all of them
     together count.  They keep their bits, because the reference follows the probabilities
-    times the values' scales, the drafts' among them.  (64 tokens a sequence and more units
-    than CTAs: the cached tile and the drafts' share a reference.)"""
+    times the values' scales, and the drafts (of scale 1) come after it.  (64 tokens a
+    sequence and more units than CTAs: a CTA has the cached tile and the drafts' in turn.)"""
     n, T, h, d = (48, 64, 4, 64) if lead == "drafts" else (1, 2000, 2, 64)
     c = case([0] * n, h, h, d, [16], vb, asym, room=T)
     for z in range(n):
