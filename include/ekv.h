@@ -489,7 +489,7 @@ EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t 
  *   k, v        the same with [Hkv][d]; strides in elements, multiples of 8, at
  *               least a token's heads; bases 16-byte aligned; o overlaps none of q, k, v
  * o_ih = sum_{j <= i} softmax_j(scale q_ih . k_jg) v_jg over i's sequence,
- * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d).  fp32 accumulation, the
+ * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d), at most 2^127.  fp32 accumulation, the
  * probabilities rounded to fp16 before they multiply V, o rounded to fp16 (RNE).
  * head_dim 64 or 128 (else EKV_EUNSUPPORTED).  total_tokens: rows of every
  * buffer; bounds outside [0, total_tokens] or descending leave that sequence out.

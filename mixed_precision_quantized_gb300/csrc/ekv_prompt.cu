@@ -343,7 +343,7 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
       int mt, h;
       if (!cur.tile(A, tb, t, mt, h)) continue;
       const int nk = mt + 1;
-      float mref = -CUDART_INF_F;
+      float xref = 0.f;  // the score that the reference m = sigma log2(e) xref goes by
       uint64_t l2 = pack2(0.f, 0.f);
       bool ok = !*stop;
       for (int j = 0; j < nk && ok; ++j) {
@@ -368,14 +368,14 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
           for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], fmaxf(x[c + 2 * u], x[c + 2 * u + 1]));
 #pragma unroll
         for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[124 + u]);
-        const float mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * A.sl;
-        const bool move = j == 0 || mnew > mref + SLACK;
+        const float xnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool move = (xnew - xref) * A.sl > SLACK;
         if (j == 0) {
-          mref = mnew;
+          xref = xnew;
         } else if (__any_sync(0xffffffffu, move)) {
           // O holds the products up to tile j - 1: wait for them, rescale this row
-          const float f = move ? ex2(mref - mnew) : 1.f;
-          if (move) mref = mnew;
+          const float f = move ? ex2((xref - xnew) * A.sl) : 1.f;
+          if (move) xref = xnew;
           ok = warp_wait(o_done + 8 * t, oph ^ 1, stop);
           if (!ok) break;
           fence_after();
@@ -390,7 +390,15 @@ prompt_kernel(PromptArgs A, const __grid_constant__ CUtensorMap mq,
             tmem_st32(to + 32 * c, r);
           }
         }
-        const uint64_t sl2 = pack2(A.sl, A.sl), mm = pack2(BOOST - mref, BOOST - mref);
+        // Past 2^22 the rounding of m would show in the exponent (at 2^27 as infinite
+        // probabilities): the differences are taken before the scale then.
+        float off = BOOST - xref * A.sl;
+        if (__any_sync(0xffffffffu, fabsf(xref * A.sl) >= 0x1p22f)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] -= xref;
+          off = BOOST;
+        }
+        const uint64_t sl2 = pack2(A.sl, A.sl), mm = pack2(off, off);
         uint32_t p[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
@@ -511,7 +519,7 @@ extern "C" EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, in
                                        int64_t v_stride, void* o, int64_t o_stride, void* stream) {
   using namespace ekv;
   if (n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads || n_q_heads > 4096 ||
-      total_tokens < 0 || n_seqs < 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.0e38f)
+      total_tokens < 0 || n_seqs < 0 || !(softmax_scale >= 0.f) || softmax_scale > 0x1p127f)
     return EKV_EINVAL;
   if (head_dim != 64 && head_dim != 128) return EKV_EUNSUPPORTED;
   if (total_tokens == 0 || n_seqs == 0) return EKV_OK;

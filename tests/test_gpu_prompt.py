@@ -172,6 +172,36 @@ def test_large_logits_and_equal_rows(d):
     assert torch.all(ekv.prompt_attn(q, k, v, cu) == 65504)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [100, 3000, 10000, 30000, 65504])
+def test_largest_logits(size, d):
+    """Logits up to fp16's end squared times d: equal keys give the mean of their values,
+    opposite ones nothing; keys that rise by steps give each row its own value.  Equal
+    scores have equal probabilities 2^(7 + e), e the reference's rounding; their rounding to
+    fp16 (2^-11) is in the products and not in the row sum, so it stays: with the output's
+    own rounding and n of 2^-23 for the sums, 2^-11 (|o| + mean |v|) + n 2^-23 mean |v|."""
+    T = 300
+    g = torch.Generator(device="cuda").manual_seed(d)
+    row = torch.sign(torch.randn(1, 1, d, generator=g, device="cuda")).half() * size
+    q, k = row.repeat(T, 2, 1), row.repeat(T, 1, 1)
+    v = torch.randn(T, 1, d, generator=g, device="cuda").half()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    live = torch.ones(T, 1, 1, dtype=torch.float64, device="cuda")
+    for step in (None, 7):
+        if step:
+            k[step::step] *= -1
+            live[step::step] = 0
+        o = ekv.prompt_attn(q, k, v, cu).double()
+        n = live.cumsum(0)
+        want, size_v = (live * v.double()).cumsum(0) / n, (live * v.double().abs()).cumsum(0) / n
+        assert torch.all((o - want).abs() <= 2.0 ** -11 * (want.abs() + size_v) +
+                         T * 2.0 ** -23 * size_v)
+    if size >= 3000:  # steps of 1 in 2^10 of the logit, far above one
+        k = row * (0.5 + torch.arange(T, device="cuda").view(T, 1, 1) * 2.0 ** -10).half()
+        assert torch.equal(ekv.prompt_attn(q, k, v, cu), v.expand(T, 2, d))
+        assert torch.equal(ekv.prompt_attn(q, k, v, cu, softmax_scale=2.0 ** 126), v.expand(T, 2, d))
+
+
 def test_rising_maximum():
     """Each key's logit is far above all before it, then far below: the running
     maximum moves at every key, and a late row's first keys vanish."""

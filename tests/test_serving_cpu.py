@@ -120,6 +120,11 @@ def test_prompt_refuses(ekv, kw):
     assert ekv.lib().ekv_prompt_attn(*_prompt_args(**kw)) == EINVAL
 
 
+def test_prompt_refuses_scales_whose_product_with_log2e_overflows(ekv):
+    for scale in (2.4e38, 3.0e38):
+        assert ekv.lib().ekv_prompt_attn(*_prompt_args(scale=scale)) == EINVAL
+
+
 def test_prompt_head_dim_and_nothing(ekv):
     assert ekv.lib().ekv_prompt_attn(*_prompt_args(d=96)) == EUNSUPPORTED
     assert ekv.lib().ekv_prompt_attn(*_prompt_args(total=0)) == 0
