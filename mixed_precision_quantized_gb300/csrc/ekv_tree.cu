@@ -150,7 +150,7 @@ struct TreeArgs {
   const __half *q, *k, *v;
   __half* o;
   float* acc;       // [2 grid][D / 4][128] float4
-  float2* ml;       // [2 grid][128] (max, sum)
+  float2* ml;       // [2 grid][128] (reference score, sum)
   int64_t* pre;     // for the merging kernel: [n_seqs + 1], then the runs' starts [grid + 1]
   int grid;
   float q_ext, k_ext;  // Q's constant c for the log2 s channels, and 1 / (sl c)
@@ -563,6 +563,21 @@ __device__ __forceinline__ void unpack_role(const DevState& st, const TreeArgs& 
   }
 }
 
+// A warp's scores at ts become their differences from each row's xref (out of line: in the
+// loop of the softmax, where it hardly ever runs, it costs 1.3 us a call at tree_chain).
+__device__ __noinline__ void far_scores(uint32_t ts, float xref) {
+#pragma unroll 1
+  for (int c = 0; c < TN; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(ts + c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) - xref);
+    tmem_st16(ts + c, v);
+  }
+  tmem_wait_st();
+}
+
 template <int D, bool ASYM>
 __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
   using Cfg = TCfg<D>;
@@ -932,7 +947,9 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       if (lane == 0) bar_arrive(q_full);
       asm volatile("bar.sync 1, 256;" ::: "memory");  // anc is there
 
-      float mref = NONE;
+      float xref = NONE;  // the score that the reference m = sigma log2(e) xref goes by
+      float boost = BOOST;  // 7 - m
+      bool far = false;
       uint64_t l2 = pack2(0.f, 0.f), z2 = pack2(0.f, 0.f);
       const int n = w.e - w.s;
 #pragma unroll 1
@@ -950,7 +967,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
         const uint64_t sl2 = pack2(st.scale_log2, st.scale_log2);
         unsigned long long seen = ~0ull;
         bool part = false;
-        float mnew = -CUDART_INF_F;
+        float xnew = -CUDART_INF_F;
         // Scores are read from tensor memory twice, 32 columns at a time (short loops
         // keep the roles' code within the instruction caches).
         if (have && ok) {
@@ -973,22 +990,27 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
             for (int c = 0; c < 32; c += 2)
               mx[c >> 1 & 3] = fmaxf(mx[c >> 1 & 3], fmaxf(x[c], x[c + 1]));
           }
-          mnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * st.scale_log2;
+          xnew = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
         int moves;
         asm volatile(
             "{ .reg .pred p, q; setp.ne.s32 p, %1, 0; "
             "barrier.cta.red.or.pred.aligned q, 2, 256, p; selp.s32 %0, 1, 0, q; }"
             : "=r"(moves)
-            : "r"((int)(mnew > mref + SLACK))
+            : "r"((int)((xnew - xref) * st.scale_log2 > SLACK))
             : "memory");
         if (moves) {  // some row's reference moves
-          M.mx[t][row] = mnew;
+          M.mx[t][row] = xnew;
           asm volatile("bar.sync 1, 256;" ::: "memory");
-          mnew = fmaxf(mnew, M.mx[t ^ 1][row]);
-          const bool move = mnew > mref + SLACK;
-          const float f = move ? ex2(mref - mnew) : 1.f;
-          if (move) mref = mnew;
+          xnew = fmaxf(xnew, M.mx[t ^ 1][row]);
+          const bool move = (xnew - xref) * st.scale_log2 > SLACK;
+          const float f = move ? ex2((xref - xnew) * st.scale_log2) : 1.f;
+          if (move) xref = xnew;
+          // Past 2^22 the rounding of m would show in the exponent (at 2^24 as infinite
+          // probabilities): the differences are taken before the scale then.
+          const float m = xref * st.scale_log2;
+          far = __any_sync(0xffffffffu, fabsf(m) >= 0x1p22f);
+          boost = far ? BOOST : BOOST - m;
           l2 = fma2(l2, pack2(f, f), pack2(0.f, 0.f));
           if (ASYM) z2 = fma2(z2, pack2(f, f), pack2(0.f, 0.f));
           if (x0 > 0 && ok) {  // O holds the products up to the pair before: rescale it
@@ -1013,7 +1035,8 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
           fence_after();
         }
         if (have && ok) {
-          const uint64_t off = pack2(BOOST - mref, BOOST - mref);
+          if (far) far_scores(ts, xref);
+          const uint64_t off = pack2(boost, boost);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             float x[32];
@@ -1074,7 +1097,7 @@ __global__ void __launch_bounds__(TT, 1) tree_kernel(DevState st, TreeArgs A) {
       const bool direct = w.whole();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       float4* part4 = reinterpret_cast<float4*>(A.acc) + (size_t)w.slot * (D / 4) * TM_ROWS;
-      if (!direct && mine && t == 0) A.ml[(size_t)w.slot * TM_ROWS + row] = make_float2(mref, l);
+      if (!direct && mine && t == 0) A.ml[(size_t)w.slot * TM_ROWS + row] = make_float2(xref, l);
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t x[16];
@@ -1191,7 +1214,7 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float f = ml[u].y > 0.f ? ex2(ml[u].x - m) : 0.f;
+        const float f = ml[u].y > 0.f ? ex2((ml[u].x - m) * st.scale_log2) : 0.f;
         l = fmaf(f, ml[u].y, l);
         v.x = fmaf(f, x[u].x, v.x);
         v.y = fmaf(f, x[u].y, v.y);

@@ -307,6 +307,39 @@ def test_draft_values_of_every_size(case, asym, vb, d, m):
     c.attend(q, kd, vd, par)
 
 
+@pytest.mark.parametrize("vb", [4, 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("size", [100, 3000, 10000, 30000, 65504])
+def test_largest_logits(case, vb, d, T, size):
+    """Logits up to fp16's end squared times d, in one CTA's run and in many: equal keys
+    give the mean of their values, opposite ones (a third of the cached, and the node's
+    own) nothing, as with decode attention; the values' scales are all one (a score of this
+    size leaves no bits for them).  Equal scores have equal probabilities up to the
+    exponent's rounding, whose rounding to fp16 (2^-11) is in the products and not in the
+    row sum: 2^-11 (|o| + mean |v|), and T of 2^-23 for the sums."""
+    rng = np.random.default_rng(d)
+    c = case([0], 2, 1, d, [16], vb, room=T)
+    row = np.sign(rng.normal(size=(1, 1, d))).astype(np.float16) * np.float16(size)
+    k, v = np.repeat(row, T, 0), rng.uniform(-1, 1, size=(T, 1, d)).astype(np.float16)
+    v[:, :, 5] = 1
+    k[1::3] *= -1
+    c.refill(k, v, 16)
+    live = np.ones((T, 1))
+    live[1::3] = 0
+    vh = c.state[0].vhat().astype(np.float64)[:, 0]
+    want = (live * vh).sum(0) / live.sum()
+    mean = (live * np.abs(vh)).sum(0) / live.sum()
+    q = torch.from_numpy(np.repeat(row[None], 2, 2)).cuda()
+    kd, vd = torch.from_numpy(-row[None]).cuda(), torch.from_numpy(v[None, :1]).cuda()
+    o = c.cache.tree_attn(0, c.slots, q, kd, vd, torch.full((1, 1), -1, dtype=torch.int32).cuda())
+    b = c.cache.decode_attn(0, c.slots, q[:, 0].contiguous()).double().cpu().numpy()
+    c.cache.sync()
+    o = o[0, 0].double().cpu().numpy()
+    assert np.all(np.abs(o - want) <= 2.0 ** -11 * (np.abs(want) + mean) + T * 2.0 ** -23 * mean)
+    assert np.all(np.abs(b[0] - want) <= 2e-3 + 1e-2 * np.abs(want))
+
+
 def test_more_sequences_than_one_launch_takes(case):
     """300 sequences of 0 to 40 tokens (a launch takes 256)."""
     lens = np.random.default_rng(2).integers(0, 41, 300).tolist()
