@@ -1155,12 +1155,14 @@ __global__ void __launch_bounds__(TM_ROWS) tree_merge_kernel(DevState st, TreeAr
                                                              int groups) {
   __shared__ int64_t s_start[MAX_GRID + 1];
   __shared__ int s_slot[MAX_GRID];
+  // Every CTA, also one without rows: the scratch that tree_kernel wrote is free for other work
+  // once this launch is over.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rt = blockIdx.x % rt_max, h = blockIdx.x / rt_max % st.Hkv;
   const int z = blockIdx.x / rt_max / st.Hkv, row = threadIdx.x;
   const int cnt = A.n_nodes ? min(A.m, max(0, A.n_nodes[z])) : A.m;
   const int rows = rows_of(cnt, st.G);
   if (rt * TM_ROWS >= rows) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = row; i <= A.grid; i += TM_ROWS) s_start[i] = A.pre[A.n_seqs + 1 + i];
   // The runs that hold parts of this unit, [a, a + nt): c0 .. c1 - 1.
   const int64_t first = A.pre[z], units = (int64_t)st.Hkv * row_tiles(rows);

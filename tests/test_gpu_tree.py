@@ -340,6 +340,21 @@ def test_largest_logits(case, vb, d, T, size):
     assert np.all(np.abs(b[0] - want) <= 2e-3 + 1e-2 * np.abs(want))
 
 
+def test_trees_of_no_nodes_leave_everything(case):
+    """Counts of 0 for every sequence (no unit, so no part to merge), then the scratch's
+    memory goes to the next tensors: they hold what is written to them."""
+    c = case([300, 20], 8, 2, 128, [4], 4)
+    q, k, v, par = c.drafts(9)
+    out = torch.full_like(q, 5.0)
+    none = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for i in range(20):
+        c.cache.tree_attn(0, c.slots, q, k, v, torch.from_numpy(par).cuda(), n_nodes=none, out=out)
+        fill = [torch.full((1 << 22,), i, dtype=torch.int32, device="cuda") for _ in range(3)]
+        assert all(torch.all(f == i) for f in fill)
+    c.cache.sync()
+    assert torch.all(out == 5.0)
+
+
 def test_more_sequences_than_one_launch_takes(case):
     """300 sequences of 0 to 40 tokens (a launch takes 256)."""
     lens = np.random.default_rng(2).integers(0, 41, 300).tolist()
