@@ -550,8 +550,8 @@ EKV_API int ekv_tree_attn_scratch_bytes(ekv_cache* cache, int32_t n_seqs, int32_
  *   u_accept      dev fp32 [n_seqs][max_nodes] in [0, 1); u_sample [n_seqs]
  *   path          dev int32 [n_seqs][max_nodes]: accepted nodes in order, then -1
  *   n_accept, next_token  dev int32 [n_seqs] (0 and -1 where n_nodes <= 0)
- * Entries of a row count as fixed point in units of 2^-60, clamped to [0, 1] (NaN
- * as 0); a row must sum to less than 4. */
+ * Entries of a row count clamped to [0, 1] (NaN as 0), in sums as fixed point in units of
+ * 2^-60; a row must sum to less than 4. */
 EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_t vocab,
                             const float* target_probs, int64_t target_seq_stride,
                             int64_t target_row_stride, const float* draft_probs,

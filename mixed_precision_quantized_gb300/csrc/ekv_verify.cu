@@ -48,11 +48,12 @@ struct VerifyArgs {
   int m, vocab;
 };
 
-// 2^60 x for x in [0, 1] (clamped; negative and NaN: 0), truncated: the 24-bit mantissa
-// shifted to its place (the conversion instruction to 64 bits runs at a fraction of the
-// rate of the shifts).
+// An entry of a row as it counts: clamped to [0, 1], NaN as 0.
+__device__ __forceinline__ float entry(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+// 2^60 of an entry, truncated: the 24-bit mantissa shifted to its place (the conversion
+// instruction to 64 bits runs at a fraction of the rate of the shifts).
 __device__ __forceinline__ uint64_t fix60(float x) {
-  x = x > 0.f ? fminf(x, 1.f) : 0.f;
+  x = entry(x);
   const uint32_t bits = __float_as_uint(x);
   const int up = (int)(bits >> 23) - 90;  // x = m 2^(e - 150)
   const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u;
@@ -135,8 +136,8 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
       s_par[tid] = ok ? par : -1;
       s_tok[tid] = tok;
       s_u[tid] = A.u[(size_t)z * A.m + tid];
-      s_p[tid] = ok ? P[par * A.p_row + tok] : 0.f;
-      s_q[tid] = ok && Q ? Q[par * A.q_row + tok] : 1.f;
+      s_p[tid] = ok ? entry(P[par * A.p_row + tok]) : 0.f;
+      s_q[tid] = ok && Q ? entry(Q[par * A.q_row + tok]) : 1.f;
     }
   }
   __syncthreads();

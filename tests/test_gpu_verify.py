@@ -148,6 +148,29 @@ def test_negative_nan_and_small_entries():
         assert nxt.item() == want
 
 
+@pytest.mark.parametrize("V", [8, 9000])
+@pytest.mark.parametrize("bad", [np.nan, -np.inf, -3.0, 1.5, np.inf])
+@pytest.mark.parametrize("draft", [False, True], ids=["target", "draft"])
+def test_entries_outside_0_to_1_at_drafted_tokens(draft, bad, V):
+    """A drafted token's own p (and q) may be such an entry: the tests of it and of its
+    siblings go by the clamped value, as the sums do."""
+    m = 4
+    p = np.zeros((6, m, V), np.float32)
+    p[:, :, :5] = [0.5, 0.125, 0.125, 0.125, 0.125]
+    q = np.roll(p, 1, -1) + 2.0 ** -10
+    par = np.tile(np.array([-1, 0, 0, 0], np.int32), (6, 1))
+    tok = np.tile(np.array([0, 1, 2, 0], np.int32), (6, 1))
+    p[:, :, 1] = bad
+    q[3:, :, 2] = bad
+    clean = lambda x: np.clip(np.nan_to_num(x, nan=0.0, posinf=1.0, neginf=0.0), 0, 1)  # noqa: E731
+    for uu in (0.05, 0.11, 0.4, 0.95):
+        u, us = np.full((6, m), uu, np.float32), np.linspace(0, 0.99, 6).astype(np.float32)
+        a = [ekv.verify_tree(*_dev(x, tok, par, u, us), draft_probs=_dev(y if draft else None)[0])
+             for x, y in ((p, q), (clean(p), clean(q)))]
+        assert all(torch.equal(x, y) for x, y in zip(*a))
+        _check(clean(p), clean(q) if draft else None, tok, par, u, us)
+
+
 def test_strided_views_and_streams():
     """Rows inside a wider buffer (odd and aligned strides), another stream, and a
     captured graph replayed on new numbers."""
