@@ -543,7 +543,8 @@ EKV_API int ekv_tree_attn_scratch_bytes(ekv_cache* cache, int32_t n_seqs, int32_
  * cum_i(r) > u_sample sum(r) (r = p_u if sum(r) is 0).
  *   target_probs  dev fp32: p after node i of sequence z at
  *                 z * target_seq_stride + i * target_row_stride, [vocab] (strides
- *                 in elements; row stride >= vocab); draft_probs likewise or NULL
+ *                 in elements; row stride >= vocab; vocab at most 2^30); draft_probs
+ *                 likewise or NULL
  *   tokens, parents  dev int32 [n_seqs][max_nodes] (tokens[z][0] is not used);
  *                 a token outside the vocabulary is never accepted
  *   n_nodes       dev int32[n_seqs] or NULL (max_nodes each)

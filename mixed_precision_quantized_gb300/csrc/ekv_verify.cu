@@ -390,7 +390,7 @@ extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_
                                        int32_t* next_token, void* stream) {
   using namespace ekv;
   if (n_seqs < 0 || n_seqs > (1 << 20) || max_nodes < 1 || max_nodes > EKV_TREE_MAX_NODES ||
-      vocab < 1)
+      vocab < 1 || vocab > (1 << 30))  // (entries are counted in int, a few units past the end)
     return EKV_EINVAL;
   if (n_seqs == 0) return EKV_OK;
   if (!target_probs || !tokens || !parents || !u_accept || !u_sample || !path || !n_accept ||

@@ -146,6 +146,11 @@ def test_verify_refuses(ekv, kw):
     assert ekv.lib().ekv_verify_tree(*_verify_args(**kw)) == EINVAL
 
 
+@pytest.mark.parametrize("V", [(1 << 30) + 1, (1 << 31) - 1])
+def test_verify_refuses_rows_past_its_index_arithmetic(ekv, V):
+    assert ekv.lib().ekv_verify_tree(*_verify_args(V=V, ps=4 * V, pr=V)) == EINVAL
+
+
 def test_verify_of_nothing_is_ok(ekv):
     assert ekv.lib().ekv_verify_tree(*_verify_args(n=0)) == 0
 
