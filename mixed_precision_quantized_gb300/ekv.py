@@ -217,6 +217,8 @@ class _Here:
 
 def _on(index: int, stream):
     if stream is not None or torch._C._cuda_getDevice() != index:
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the call's tensors on cuda:{index}")
         return _On(index, stream)
     h = _Here()
     h.handle = torch._C._cuda_getCurrentRawStream(index)

@@ -176,6 +176,16 @@ def test_binding_refuses_cpu_tensors_types_and_shapes(ekv):
         ekv.prompt_attn(h.float(), h, h, cu)
 
 
+def test_binding_refuses_a_stream_of_another_gpu(ekv):
+    """The call runs where its tensors are; a stream elsewhere is not replaced by one there."""
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError, match="stream"):
+        ekv._on(0, Stream())
+
+
 def test_oracle_attention_and_tree():
     """Two keys of equal logits average; a chain's node sees its prefix, a tree's only
     its ancestors; a row that sees nothing is zero."""
