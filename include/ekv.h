@@ -453,13 +453,13 @@ typedef struct ekv_rope_config {
   int32_t layout;          /* EKV_ROPE_HALF or EKV_ROPE_INTERLEAVED                    */
   int32_t scaling;         /* EKV_ROPE_SCALE_*                                         */
   double base;             /* > 1                                                      */
-  double factor;           /* > 0; used by every scaling but NONE                      */
+  double factor;           /* >= DBL_MIN; used by every scaling but NONE               */
   double original_len;     /* > 0; BANDED and YARN                                     */
   double low_freq_factor;  /* > 0; BANDED                                              */
   double high_freq_factor; /* > low_freq_factor; BANDED                                */
   double beta_fast;        /* > beta_slow; YARN                                        */
   double beta_slow;        /* > 0; YARN                                                */
-  double magnitude;        /* >= 0; 0 = the scaling's own                              */
+  double magnitude;        /* 0 .. FLT_MAX; 0 = the scaling's own                      */
 } ekv_rope_config;
 
 /* The frequency table of a configuration (host only): turns[i] (host

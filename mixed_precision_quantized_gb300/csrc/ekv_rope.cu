@@ -22,6 +22,7 @@
 // of a plain copy); a thread that found its (token, head, unit) by division for every 16
 // bytes took 164.  4,099 tokens of 72 heads read from a fused projection: 33 us; with 2
 // tokens a CTA instead of 4 it takes 35.
+#include <float.h>
 #include <math.h>
 
 #include "ekv_internal.h"
@@ -158,8 +159,9 @@ bool valid_config(const ekv_rope_config* c) {
   if (c->layout != EKV_ROPE_HALF && c->layout != EKV_ROPE_INTERLEAVED) return false;
   if (c->scaling < EKV_ROPE_SCALE_NONE || c->scaling > EKV_ROPE_SCALE_YARN) return false;
   if (!(c->base > 1.0) || !isfinite(c->base)) return false;
-  if (!(c->magnitude >= 0.0) || !isfinite(c->magnitude)) return false;
-  if (c->scaling != EKV_ROPE_SCALE_NONE && (!(c->factor > 0.0) || !isfinite(c->factor)))
+  if (!(c->magnitude >= 0.0 && c->magnitude <= FLT_MAX)) return false;
+  // (below DBL_MIN a frequency over it may be infinite)
+  if (c->scaling != EKV_ROPE_SCALE_NONE && (!(c->factor >= DBL_MIN) || !isfinite(c->factor)))
     return false;
   if (c->scaling == EKV_ROPE_SCALE_BANDED || c->scaling == EKV_ROPE_SCALE_YARN) {
     if (!(c->original_len > 0.0) || !isfinite(c->original_len)) return false;

@@ -72,6 +72,19 @@ def test_rope_refuses_bad_configurations(ekv, kw):
     assert e.value.code == EINVAL
 
 
+@pytest.mark.parametrize("kw", [
+    dict(magnitude=1e39), dict(scaling="linear", factor=1e-310),
+    dict(scaling="banded", factor=5e-324, original_len=8192),
+    dict(scaling="yarn", factor=1e-309, original_len=8192)])
+def test_rope_refuses_what_no_float_holds(ekv, kw):
+    """A magnitude past fp32; a factor whose inverse is infinite (no frequency table)."""
+    with pytest.raises(ekv.EkvError) as e:
+        ekv.Rope(128, device="cpu", **kw)
+    assert e.value.code == EINVAL
+    r = ekv.Rope(128, device="cpu", scaling="linear", factor=1e-300)
+    assert all(0 <= t < 1 << 64 for t in r.turns)
+
+
 def test_rope_refuses_unknown_names(ekv):
     with pytest.raises(ValueError):
         ekv.Rope(128, layout="rows", device="cpu")
