@@ -1254,9 +1254,11 @@ cudaError_t launch_tree(const DevState& st, TreeArgs A, int n_seqs, cudaStream_t
     tree_kernel<D, ASYM><<<A.grid, TT, tree_smem<D>(), s>>>(st, A);
     e = cudaGetLastError();
     if (e != cudaSuccess) break;
-    // One thread a row and 4 channels; with many row tiles each thread takes 4 of them.
+    // One thread a row and 4 channels; with many row tiles each thread takes 4 of them.  Whole
+    // call with four and with one, us: 32 tiles 34.9 and 29.4, 64 27.1 and 23.3 (52.6 and 50.6
+    // with every row used), 128 36.3 and 36.0 (77.2 and 79.1), 256 54.1 and 56.9 (68.2, 70.6).
     const int rt_max = (rows_of(B.m, st.G) + TM_ROWS - 1) / TM_ROWS;
-    const int tiles = A.n_seqs * st.Hkv * rt_max, groups = tiles >= 64 ? 4 : 1;
+    const int tiles = A.n_seqs * st.Hkv * rt_max, groups = tiles >= 128 ? 4 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles, D / 4 / groups);
     cfg.blockDim = dim3(TM_ROWS);
