@@ -464,7 +464,7 @@ typedef struct ekv_rope_config {
 
 /* The frequency table of a configuration (host only): turns[i] (host
  * uint64[rot_dim / 2]) = f_i / 2pi as a fraction of 2^64 (whole turns dropped),
- * and the magnitude g (may be NULL). */
+ * and the magnitude g (may be NULL).  f_i is computed in double. */
 EKV_API int ekv_rope_table(const ekv_rope_config* cfg, uint64_t* turns, float* magnitude);
 
 /* Rotate q and k of n_tokens tokens.
@@ -474,8 +474,9 @@ EKV_API int ekv_rope_table(const ekv_rope_config* cfg, uint64_t* turns, float* m
  *              (strides in elements, >= Hq * d, multiples of 8; bases 16-byte
  *              aligned).  q_out may be q itself (same stride: in place); the
  *              buffers must not overlap otherwise.  k, k_out: the same.
- * A head count of 0 leaves that tensor out.  Angles are exact to 2^-32 turns at
- * every position; the rotation is fp32, rounded once to fp16 (RNE). */
+ * A head count of 0 leaves that tensor out.  Angles are within 2^-26 turns (their
+ * conversion to fp32) and, where f_i <= 1, |position| 2^-53 (the table's double f_i) of
+ * their formula; the rotation is fp32, rounded once to fp16 (RNE). */
 EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t n_tokens,
                      const int32_t* positions, int32_t n_q_heads, const void* q, int64_t q_stride,
                      void* q_out, int64_t q_out_stride, int32_t n_kv_heads, const void* k,
@@ -492,7 +493,10 @@ EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t 
  * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d), at most 2^127.  fp32 accumulation, the
  * probabilities rounded to fp16 before they multiply V, o rounded to fp16 (RNE).
  * head_dim 64 or 128 (else EKV_EUNSUPPORTED).  total_tokens: rows of every
- * buffer; bounds outside [0, total_tokens] or descending leave that sequence out.
+ * buffer; bounds outside [0, total_tokens] or descending leave that sequence out (what
+ * is left must not overlap: a row of two sequences gets either's result).  A value of a
+ * later token, though it counts nothing, must be finite too: infinities and NaN in V
+ * spread to earlier rows of the same 128 tokens.
  * The call keeps no state and takes no scratch: calls may overlap on the GPU.  A
  * bounded wait inside the kernel that gave up (it never should) leaves NaN in the
  * rows it was to write. */
@@ -511,7 +515,8 @@ EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_
  *              rows of o behind a sequence's nodes are left as they were
  *   parents    dev int32[n_seqs][max_nodes]
  *   q, o       dev fp16 [n_seqs][max_nodes][Hq][d]
- *   k, v       dev fp16 [n_seqs][max_nodes][Hkv][d]; all four 16-byte aligned
+ *   k, v       dev fp16 [n_seqs][max_nodes][Hkv][d]; all four 16-byte aligned; o overlaps
+ *              neither k nor v.  Infinities and NaN in a node's v spread to the whole tree
  * o_ih = softmax-weighted sum over every cached token of the sequence (the
  * dequantized page values, as ekv_decode_attn) and over the k, v of node i and
  * its ancestors.  A sequence may have no cached tokens.  The handle's softmax scale

@@ -7,12 +7,13 @@
 // long contexts by the configured scaling; g is the scaling's magnitude.
 //
 // The angle is kept in turns as a 64-bit fixed-point fraction: the table holds
-// F_i = round(f_i / 2pi * 2^64), and pos * F_i mod 2^64 is the fraction of a
-// turn, exact in the product for every int32 position (the table's rounding
-// moves the angle by at most 2^31 * 2^-65 turns).  Its top 32 bits go to fp32
-// and through sincospif, so a far position loses nothing to range reduction and
-// no fp64 arithmetic is spent.  The rotation is done in fp32 and rounded to
-// fp16 once.
+// F_i = f_i / 2pi * 2^64 of a double f_i, and pos * F_i mod 2^64 is the fraction
+// of a turn, exact in the product for every int32 position.  f_i <= 1 is within
+// 2^-53 turns a position of its formula (the roundings of the exponent, pow and the
+// division; 2^-55 measured), at position 131,072 within 2^-36 and at the last 2^-22.
+// The top 32 bits go to fp32 (2^-26 turns) and through sincospif, so a far position
+// loses nothing to range reduction and no fp64 arithmetic is spent.  The rotation is
+// done in fp32 and rounded to fp16 once.
 //
 // Bound by memory: each q and k element is read and written once.  A CTA takes a
 // few tokens; its threads first fill a shared table of cos and sin, one entry
@@ -31,7 +32,7 @@ namespace ekv {
 namespace {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_MAX_TOKENS = 8;   // tokens of one CTA at most
+constexpr int ROPE_MAX_TOKENS = 4;   // tokens of one CTA at most
 constexpr int ROPE_MAX_PAIRS = 64;   // head_dim / 2
 
 struct RopeArgs {
@@ -220,7 +221,7 @@ extern "C" EKV_API int ekv_rope_table(const ekv_rope_config* cfg, uint64_t* turn
   for (int i = 0; i < cfg->rot_dim / 2; ++i) {
     double t = freq_of(*cfg, i) / kTwoPi;
     t -= floor(t);  // whole turns do not matter
-    // t < 1 in doubles, so t * 2^64 < 2^64; split so that the conversion is exact
+    // t < 1 in doubles, so t * 2^64 < 2^64; split so that only bits below 2^-64 are cut
     const uint64_t hi = (uint64_t)(t * 0x1p32);
     turns[i] = (hi << 32) + (uint64_t)((t * 0x1p32 - (double)hi) * 0x1p32);
   }
@@ -263,7 +264,10 @@ extern "C" EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turn
   A.d = cfg->head_dim;
   A.rot = cfg->rot_dim;
   A.mag = magnitude_of(*cfg);
-  A.tokens = n_tokens >= 2048 ? 4 : 1;
+  // Four tokens a CTA once there are enough of them for all SMs.  Kernel time with four and with
+  // one, us: 40 heads of 128 at 256 tokens 4.3 and 3.1, 512 4.4 and 4.0, 1,024 5.8 and 6.3,
+  // 2,048 9.4 and 10.1, 32,768 114 and 149; 6 heads at 256 2.7 both, 2,048 3.9 and 7.7.
+  A.tokens = n_tokens >= 2048 ? ROPE_MAX_TOKENS : 1;
   const int64_t grid = (n_tokens + A.tokens - 1) / A.tokens;
   const bool inter = cfg->layout == EKV_ROPE_INTERLEAVED;
   const bool vec = A.rot % (inter ? 8 : 16) == 0;

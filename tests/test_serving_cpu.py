@@ -5,6 +5,7 @@ import ctypes
 import math
 import os
 import shutil
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -49,6 +50,21 @@ def test_rope_table_matches_the_formulas(ekv, kw):
     assert abs(r.magnitude - mag) <= 2 ** -23 * mag
     for t, want in zip(r.turns, f / (2 * math.pi)):
         assert abs(t * 2.0 ** -64 - want) <= 64 * 2.0 ** -53 * want + 2.0 ** -63
+
+
+@pytest.mark.parametrize("base", [1.5, 10000.0, 500000.0, 7e8])
+@pytest.mark.parametrize("rot", [2, 20, 126, 128])
+def test_rope_table_in_50_digits(ekv, base, rot):
+    """Against decimal arithmetic: within 2^-53 turns a position.  -2i/r is rounded (2^-53),
+    which moves f by f |ln f| 2^-53 <= 2^-53 / e; pow adds 2^-52 f at most, the division by
+    2 pi and 2 pi itself 2^-53 f each: (1 / e + 4) 2^-53 / 2 pi < 2^-53.4; what is cut below
+    2^-64 is nothing beside it."""
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582")
+    with localcontext() as c:
+        c.prec = 50
+        for i, t in enumerate(ekv.Rope(128, rot_dim=rot, base=base, device="cpu").turns):
+            want = (Decimal(base).ln() * Decimal(-2 * i) / Decimal(rot)).exp() / (2 * pi)
+            assert abs(Decimal(t) / 2 ** 64 - want) <= Decimal(2) ** -53
 
 
 def test_rope_magnitude_can_be_set(ekv):
