@@ -284,14 +284,12 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
     }
   }
 
-  int next = -1;
   if (cnt > 0) {
     if (!have) total = row_sum(node, k, ngone);
     if (total == 0 && (k > 0 || ngone > 0)) {
       k = ngone = 0;
       total = row_sum(node, 0, 0);
     }
-    next = V - 1;  // an all-zero row
     if (total > 0) {
       const float us = A.us[z];
       const uint64_t frac = us >= 1.f ? ~0ull : us > 0.f ? __float2ull_rz(us * 0x1p64f) : 0ull;
@@ -299,7 +297,6 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
       uint64_t base = 0;
       for (int r = 0; r < rank; ++r) base += s_part[flip ^ 1][r];
       for (int w = 0; w < warp; ++w) base += s_wsum[w];
-      next = -1;
       if (target >= base && target - base < s_wsum[warp]) {  // this warp's chunk holds it
         const float* pr = P + node * A.p_row;
         const float* qr = Q ? Q + node * A.q_row : nullptr;
@@ -356,7 +353,7 @@ __global__ void __launch_bounds__(VT, 2) verify_kernel(VerifyArgs A) {
     if (tid == 0) {
       A.n_accept[z] = nacc;
       if (cnt <= 0) A.next[z] = -1;
-      else if (total == 0) A.next[z] = V - 1;
+      else if (total == 0) A.next[z] = V - 1;  // an all-zero row
     }
   }
   if (CL > 1) cg::this_cluster().sync();  // no CTA leaves while another may write its sums
@@ -422,9 +419,11 @@ extern "C" EKV_API int ekv_verify_tree(int32_t n_seqs, int32_t max_nodes, int32_
   A.next = next_token;
   A.m = max_nodes;
   A.vocab = vocab;
-  // A cluster of 8 CTAs a sequence once a row has more than a few units a warp: 32
-  // sequences of 131,072 entries take 90 us with one CTA each and 9 with eight; at 1,024
-  // entries the cluster's barriers cost more than the row.
+  // A cluster of 8 CTAs a sequence once a row has more than a few units a warp.  Kernel time of
+  // 32 sequences of 8 nodes with eight CTAs and with one, us: 131,072 entries 14.9 and 54.0
+  // (with draft probabilities 45 and 166), 16,384 7.9 and 10.7 (21 and 31), 8,192 6.7 and 7.8
+  // (14.2 and 16.4), 4,096 6.7 and 6.2 (14.8 both), 1,024 6.6 and 4.9 (11.8 and 7.9): the
+  // cluster's barriers against the row; one sequence crosses at the same sizes.
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
       vocab > 8192 ? launch_verify<8>(A, n_seqs, s) : launch_verify<1>(A, n_seqs, s);
