@@ -491,7 +491,8 @@ EKV_API int ekv_rope(const ekv_rope_config* cfg, const uint64_t* turns, int64_t 
  *               least a token's heads; bases 16-byte aligned; o overlaps none of q, k, v
  * o_ih = sum_{j <= i} softmax_j(scale q_ih . k_jg) v_jg over i's sequence,
  * g = h / (Hq / Hkv); softmax_scale 0 -> 1/sqrt(d), at most 2^127.  fp32 accumulation, the
- * probabilities rounded to fp16 before they multiply V, o rounded to fp16 (RNE).
+ * probabilities rounded to fp16 before they multiply V (2^-11 of each; those below 2^-21
+ * of a row's largest 2^-32 of that), o rounded to fp16 (RNE).
  * head_dim 64 or 128 (else EKV_EUNSUPPORTED).  total_tokens: rows of every
  * buffer; bounds outside [0, total_tokens] or descending leave that sequence out (what
  * is left must not overlap: a row of two sequences gets either's result).  A value of a
@@ -519,7 +520,9 @@ EKV_API int ekv_prompt_attn(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_
  *              neither k nor v.  Infinities and NaN in a node's v spread to the whole tree
  * o_ih = softmax-weighted sum over every cached token of the sequence (the
  * dequantized page values, as ekv_decode_attn) and over the k, v of node i and
- * its ancestors.  A sequence may have no cached tokens.  The handle's softmax scale
+ * its ancestors.  Accuracy as ekv_prompt_attn, with a probability times its value's scale
+ * (page formats; drafts and 16-bit V: 1) in the probability's place.  A sequence may have
+ * no cached tokens.  The handle's softmax scale
  * times log2(e) lies in [2^-25, 2^15), else EKV_EUNSUPPORTED.
  *   scratch    dev, 16-byte aligned, ekv_tree_attn_scratch_bytes bytes
  *              (caller-owned; overwritten; one call at a time.  Nothing of the handle
