@@ -25,9 +25,10 @@
 // zeros in shared memory before the product, so that nothing outside a sequence (NaN,
 // infinities) reaches its rows.
 //
-// Measured: one sequence of 16,384 tokens, 32 query and 8 KV heads of 128: 1,400 us warm,
-// 1,520 with inputs that change from call to call (1.45e15 flops a second); 24 ragged
-// sequences of up to 2,047: 286 us.  The tensor cores are busy three quarters of the time at
+// Measured: one sequence of 16,384 tokens, 32 query and 8 KV heads of 128: 1,457 us warm,
+// 1,525 with inputs that change from call to call (1.44e15 flops a second), heads of 64 1,095
+// (1.0e15: the exponentials, as many for half the products); 24 ragged sequences of up to
+// 2,047: 298 us.  The tensor cores are busy three quarters of the time at
 // 16K tokens and half of it at 4K; what is left is the chain from scores to probabilities to
 // products at each item's ends.  Tried and slower: one loop of mixed steps for the two tiles'
 // products (1,800: the operands' addresses are worked out between wait and issue), scores

@@ -19,8 +19,8 @@
 // few tokens; its threads first fill a shared table of cos and sin, one entry
 // per (token, pair), which all q and k heads of the token share, then rotate
 // 8 pairs (half layout) or 4 pairs (interleaved) per step in 16-byte accesses.
-// Measured: 32,768 tokens of 48 heads of 128, interleaved, 134.5 us (805 MB: 5.99 TB/s, 0.88
-// of a plain copy); a thread that found its (token, head, unit) by division for every 16
+// Measured: 32,768 tokens of 48 heads of 128, interleaved, 133 us (805 MB: 6.05 TB/s, 0.89
+// of a plain copy), one pair at a time (a rotated part that the vectors do not fit) 569; a thread that found its (token, head, unit) by division for every 16
 // bytes took 164.  4,099 tokens of 72 heads read from a fused projection: 33 us; with 2
 // tokens a CTA instead of 4 it takes 35.
 #include <float.h>

@@ -27,11 +27,12 @@
 //                an OR over the 256 threads tells whether any row's reference has to move,
 //                which is seldom.
 //
-// What bounds it is instruction issue: a 64-token tile takes about 4,300 warp instructions
+// What bounds it is instruction issue: a 64-token tile takes about 4,400 warp instructions
 // (K 1,000, V 500, softmax 1,200 at 128 rows, the rest waits and bookkeeping of the roles)
 // at 0.58 a cycle and scheduler, while the tensor cores are busy 40% of the time and DRAM
-// 18%.  Measured at 131,072 tokens, 8 KV heads, 128 rows, 4-bit K and V: 119 us with the
-// merging kernel (154 MB: 1.29 TB/s).  Tried and slower: 16 unpacking warps (128 us: more
+// 18%.  Measured at 131,072 tokens, 8 KV heads, 128 rows, 4-bit K and V: 121 us with the
+// merging kernel (154 MB: 1.27 TB/s); asymmetric 164, 16-bit K and V 130 (537 MB: 4.1 TB/s),
+// head size 64 105.  Tried and slower (against 119): 16 unpacking warps (128 us: more
 // waits to issue), half a page a warp (136), unrolled unpacking or softmax loops (121, 124:
 // the code of 20 warps in different roles outgrows the instruction caches; the stall for
 // instructions was the largest of all until the loops were short), V scales read by each

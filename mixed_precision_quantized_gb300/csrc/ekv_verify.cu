@@ -22,9 +22,10 @@
 // one launch, one round of gathers, one pass over the last row.  A cluster of CL
 // CTAs shares a sequence's row passes, exchanging partial sums through distributed
 // shared memory (no CTA writes another's before a cluster barrier has shown that it runs,
-// and none leaves while another may write its own).  Measured: 32 trees of 64 nodes over 131,072 tokens 19 us a call (the
-// host's share is as long), 16 sampled trees of 16 over 100,003 with draft probabilities 29
-// (two to three passes at the nodes with rejections, ~3 us each).
+// and none leaves while another may write its own).  Measured: 32 trees of 64 nodes over
+// 131,072 tokens 22 us a call (the host's share is as long), 16 sampled trees of 16 over
+// 100,003 with draft probabilities 26 to 34 (two to three passes at the nodes with
+// rejections, ~3 us each).
 #include <cooperative_groups.h>
 
 #include "ekv_internal.h"
