@@ -26,11 +26,11 @@ class Case:
     run of tokens each), and its oracle."""
 
     def __init__(self, lens, hq, hkv, d, kbits, vb, asym=False, seed=0, gain=8.0, slots=None,
-                 max_seqs=None, v_scale=1.0, room=16):
+                 max_seqs=None, v_scale=1.0, room=0):
         self.lens, self.hq, self.hkv, self.d, self.vb, self.asym = lens, hq, hkv, d, vb, asym
         self.rng = np.random.default_rng(seed)
         pages = sum(-(-max(t, room) // 16) + len(kbits) for t in lens) * hkv + 1
-        self.cache = ekv.Cache(1, max_seqs or len(lens), hq, hkv, d, max(max(lens), room),
+        self.cache = ekv.Cache(1, max_seqs or len(lens), hq, hkv, d, max(max(lens), 16, room),
                                {(b, vb): pages for b in set(kbits)}, [kbits[0]], [vb], asym=asym)
         self.order = list(range(len(lens))) if slots is None else slots
         self.slots = torch.tensor(self.order, dtype=torch.int32, device="cuda")
